@@ -30,7 +30,8 @@
  *     be 16-byte aligned (RTP_EINVAL otherwise, before anything is enqueued).
  *
  * Also: the causal prefill of a prompt (rtp_prefill, same paper §3.2: dense for retrieval heads,
- * sinks + window for local heads) on the fifth-generation tensor cores.
+ * sinks + window for local heads) on the fifth-generation tensor cores; and the same layer over
+ * a paged cache (rtp_paged_*): page reservation, append, decode step.
  */
 #ifndef RTP_H
 #define RTP_H
@@ -209,6 +210,135 @@ int rtp_prefill(const rtp_layer_desc* desc, const uint16_t* q_pre, const uint16_
                 const uint16_t* v, const int32_t* n_b, int32_t n_max, uint16_t* out, void* ws,
                 size_t ws_bytes, rtp_stream_t stream);
 
+/*
+ * Paged caches. The K/V rows of all sequences of a batch live in pages of page_size tokens that
+ * a block table hands out, instead of one reserved range per sequence: rtp_paged_reserve keeps
+ * the block tables and slot maps on the GPU, rtp_paged_append_kv writes new tokens,
+ * rtp_paged_decode_step attends to them. (The pages of the sources describe no paging; the
+ * retrieval / local split of the heads is paper text §3.2, with dense attention for the
+ * retrieval heads as in rtp_prefill.)
+ *
+ * Row of token n of sequence b, KV head g: page block_table[b][n / page_size], row
+ * g * page_size + n % page_size of that page. All KV heads of a layer, local ones too, keep every
+ * position (a local head reads its sinks and window only). A slot is page * page_size + row.
+ * Entries of block_table behind a sequence's last page are not read. Several sequences may
+ * share pages (a common prefix) as long as no call writes to a shared page.
+ */
+enum {
+  RTP_KV_BF16 = 0,      /* rows of 128 bf16 */
+  RTP_KV_E4M3 = 1       /* rows of 128 e4m3 bytes and a float scale: value = byte * scale */
+};
+
+typedef struct {
+  int32_t kv_type;        /* RTP_KV_* */
+  int32_t page_size;      /* tokens per page: 16, 32, 64, 128 or 256 */
+  int32_t n_pages;        /* n_pages * page_size <= 2^31 - 1 */
+  int32_t table_stride;   /* entries per row of block_table, >= 1 */
+  void* k;                /* [n_pages][Hkv][page_size][128]: RoPE'd keys */
+  void* v;                /* [n_pages][Hkv][page_size][128]: values */
+  float* k_scale;         /* [n_pages][Hkv][page_size], RTP_KV_E4M3 only; positive */
+  float* v_scale;
+  int64_t page_stride;    /* rows from a page of k (and of v) to the next, >= Hkv * page_size;
+                             0: Hkv * page_size. Lets K and V pages, or several layers', lie
+                             side by side in one allocation. The scales are always dense. */
+  const int32_t* block_table; /* [B][table_stride] page ids; unused by rtp_paged_append_kv */
+} rtp_paged_cache;
+/* k, v, k_scale and v_scale must be 16-byte aligned (RTP_EINVAL otherwise). */
+
+/* The pages of a batch: shared by the layers of a model, whose caches use the same page ids. */
+typedef struct {
+  int32_t B;              /* sequences, 1..4096 */
+  int32_t page_size;      /* as in rtp_paged_cache */
+  int32_t n_pages;
+  int32_t table_stride;   /* a sequence holds at most table_stride * page_size tokens */
+  int32_t* free_pages;    /* [n_pages]: ring of free page ids, see rtp_paged_reserve */
+  int32_t* block_table;   /* [B][table_stride] */
+} rtp_page_pool;
+
+/* First bytes of a paged workspace: the status word and the arrival counters. A workspace of
+ * this size serves rtp_paged_reserve. */
+#define RTP_PAGED_CTRL_BYTES 4096u
+
+/* Bytes of workspace rtp_paged_decode_step needs for this description (0 on a bad one); they
+ * depend on Hq / Hkv only. */
+size_t rtp_paged_workspace_bytes(const rtp_layer_desc* desc);
+
+/* Clears the status word and the counters. Call once after allocating a workspace (256-byte
+ * aligned); every call leaves the counters at zero. Calls that share a workspace must be
+ * stream-ordered, replays of captured graphs among them, and a workspace of rtp_decode_step or
+ * rtp_prefill is not one of these. */
+int rtp_paged_workspace_init(void* ws, size_t ws_bytes, rtp_stream_t stream);
+
+/*
+ * Block tables and slot maps for new lengths, on the GPU (one launch).
+ *   lens, new_lens : [B] tokens that the sequences hold now and shall hold. A sequence holds
+ *                    ceil(len / page_size) pages, the first entries of its block-table row.
+ *   counters       : [2] {head, tail}: the ring's free pages are free_pages[i % n_pages] for
+ *                    head <= i < tail. Both only grow. A new pool: all ids, {0, n_pages}.
+ *   lens_out       : [B] lengths after the call: new_lens[b] where the sequence was served,
+ *                    lens[b] where it was not.
+ *   counters_out   : [2] counters after the call.
+ *   slot_map       : [B][n_new] slots of the tokens at positions lens[b] + j, -1 behind
+ *                    lens_out[b] (NULL when n_new is 0).
+ *   ws             : RTP_PAGED_CTRL_BYTES bytes or more, initialised.
+ * A sequence that grows takes the pages it lacks from the head of the ring, in batch order; it
+ * is served when the pages lacked by it and the sequences before it do not exceed the free pages
+ * at the call's start. A sequence that shrinks (0: ends) returns its last pages to the tail, in
+ * batch order; they serve later calls.
+ * lens_out and counters_out may be lens (or new_lens) and counters themselves.
+ * A length outside [0, table_stride * page_size] leaves that sequence as it is, and counters or
+ * lengths that cannot be this pool's (more free and returned pages than n_pages) leave all as
+ * they are; both set RTP_EDEVICE in ws's status word. Running out of pages is no error.
+ */
+int rtp_paged_reserve(const rtp_page_pool* pool, const int32_t* lens, const int32_t* new_lens,
+                      const int64_t* counters, int32_t* lens_out, int64_t* counters_out,
+                      int32_t* slot_map, int32_t n_new, void* ws, size_t ws_bytes,
+                      rtp_stream_t stream);
+
+/*
+ * Writes new tokens to their slots (one launch).
+ *   k_pre, v  : bf16 [B][n_new][Hkv][128], pre-RoPE keys and values.
+ *   start_pos : [B]; token j of sequence b is at position start_pos[b] + j.
+ *   slot_map  : [B][n_new] slots, all different; a token with a negative slot is skipped.
+ *   ws        : status word (may be NULL).
+ * RTP_KV_BF16: the rows that rtp_append_kv writes, bit for bit (R(pos) k_pre evaluated in double
+ * precision, rounded once; v). RTP_KV_E4M3: with x the row in single precision (the rotated key
+ * rounded once), scale = max(max|x| / 448, 2^-126) and bytes x / scale, to nearest even.
+ * A slot outside the pages or a negative position is skipped and sets RTP_EDEVICE.
+ */
+int rtp_paged_append_kv(const rtp_layer_desc* desc, const rtp_paged_cache* cache,
+                        const uint16_t* k_pre, const uint16_t* v, const int32_t* start_pos,
+                        const int32_t* slot_map, int32_t n_new, void* ws, rtp_stream_t stream);
+
+/*
+ * Decode step of one layer over a paged cache at position m = seq_lens[b] - 1, whose token the
+ * cache holds (one launch). Retrieval KV heads (slot_of_kv >= 0) attend to every position, local
+ * ones to j < sinks and j > m - window: o = sum_j softmax(R(m) q . k_j / sqrt(128))_j v_j.
+ *   q_pre    : bf16 [B][Hq][128], pre-RoPE queries, rotated in single precision.
+ *   seq_lens : [B], 0 <= seq_lens[b] <= min(table_stride * page_size, max_seq_len). 0: an idle
+ *              place of the batch, whose outputs are zeros and lse -inf.
+ *   out      : bf16 [B][Hq][128].
+ *   lse      : float [B][Hq], log sum_j exp(z_j), or NULL.
+ *   ws       : rtp_paged_workspace_bytes(desc) bytes or more, initialised.
+ * What a page holds outside the attended positions is not used (NaN included). A non-finite
+ * value in an attended row makes the outputs of its heads non-finite.
+ * A length out of range (treated as 0) or a page id outside [0, n_pages) (its rows are left out)
+ * sets RTP_EDEVICE in ws's status word. Repeated calls give the same bits.
+ */
+int rtp_paged_decode_step(const rtp_layer_desc* desc, const rtp_paged_cache* cache,
+                          const uint16_t* q_pre, const int32_t* seq_lens, uint16_t* out,
+                          float* lse, void* ws, size_t ws_bytes, rtp_stream_t stream);
+
+/*
+ * rtp_paged_append_kv of the decode token (position seq_lens[b] - 1, slot by the block table)
+ * and rtp_paged_decode_step in one launch, with the same results.
+ *   k_new, v_new : bf16 [B][Hkv][128]. The page of the token must not be shared.
+ */
+int rtp_paged_decode_step_append(const rtp_layer_desc* desc, const rtp_paged_cache* cache,
+                                 const uint16_t* k_new, const uint16_t* v_new,
+                                 const uint16_t* q_pre, const int32_t* seq_lens, uint16_t* out,
+                                 float* lse, void* ws, size_t ws_bytes, rtp_stream_t stream);
+
 /* Size of the library-owned scratch of rtp_decode_step_static (bytes). */
 #define RTP_STATIC_SCRATCH_BYTES (16u << 20)
 
@@ -255,8 +385,9 @@ int32_t rtp_last_launch_count(void);
  *     raises an abort flag that ends the launch's other waits; the outputs of that call are
  *     undefined and its workspace must be re-initialised with rtp_workspace_init. Process-wide.
  *   rtp_debug_fail_next_call: the next call of rtp_append_kv, rtp_decode_step,
- *     rtp_decode_step_append, rtp_decode_step_topk, rtp_decode_step_static or rtp_prefill (on
- *     any thread) returns `status` (one
+ *     rtp_decode_step_append, rtp_decode_step_topk, rtp_decode_step_static, rtp_prefill or of a
+ *     paged entry point (rtp_paged_reserve, _append_kv, _decode_step, _decode_step_append), on
+ *     any thread, returns `status` (one
  *     of the negative RTP_E* codes; 0 cancels) before checking its arguments, and enqueues
  *     nothing. Process-wide, consumed by that one call.
  */

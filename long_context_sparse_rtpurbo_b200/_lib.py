@@ -16,8 +16,12 @@ EXPORTS = (
     "rtp_append_kv", "rtp_decode_step", "rtp_read_device_status", "rtp_last_launch_count",
     "rtp_decode_step_static", "rtp_decode_step_append", "rtp_decode_step_topk", "rtp_debug_set_wait_limit",
     "rtp_debug_fail_next_call", "rtp_prefill_workspace_bytes", "rtp_prefill",
+    "rtp_paged_workspace_bytes", "rtp_paged_workspace_init", "rtp_paged_reserve",
+    "rtp_paged_append_kv", "rtp_paged_decode_step", "rtp_paged_decode_step_append",
 )
 RTP_STATIC_SCRATCH_BYTES = 16 << 20
+RTP_KV_BF16, RTP_KV_E4M3 = 0, 1
+RTP_PAGED_CTRL_BYTES = 4096
 
 
 class RtpLayerDesc(ctypes.Structure):
@@ -36,6 +40,23 @@ class RtpCache(ctypes.Structure):
         ("k_loc", ctypes.c_void_p), ("v_loc", ctypes.c_void_p),
         ("seq_off", ctypes.c_void_p), ("seq_cap", ctypes.c_void_p),
         ("T_total", ctypes.c_int64),
+    ]
+
+
+class RtpPagedCache(ctypes.Structure):
+    _fields_ = [
+        ("kv_type", ctypes.c_int32), ("page_size", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+        ("table_stride", ctypes.c_int32), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+        ("page_stride", ctypes.c_int64), ("block_table", ctypes.c_void_p),
+    ]
+
+
+class RtpPagePool(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32), ("page_size", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+        ("table_stride", ctypes.c_int32), ("free_pages", ctypes.c_void_p),
+        ("block_table", ctypes.c_void_p),
     ]
 
 
@@ -76,6 +97,19 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.rtp_prefill_workspace_bytes.argtypes = [D, i32]
     lib.rtp_prefill.restype = ctypes.c_int
     lib.rtp_prefill.argtypes = [D, vp, vp, vp, vp, i32, vp, vp, sz, vp]
+    PC, PP = ctypes.POINTER(RtpPagedCache), ctypes.POINTER(RtpPagePool)
+    lib.rtp_paged_workspace_bytes.restype = sz
+    lib.rtp_paged_workspace_bytes.argtypes = [D]
+    lib.rtp_paged_workspace_init.restype = ctypes.c_int
+    lib.rtp_paged_workspace_init.argtypes = [vp, sz, vp]
+    lib.rtp_paged_reserve.restype = ctypes.c_int
+    lib.rtp_paged_reserve.argtypes = [PP, vp, vp, vp, vp, vp, vp, i32, vp, sz, vp]
+    lib.rtp_paged_append_kv.restype = ctypes.c_int
+    lib.rtp_paged_append_kv.argtypes = [D, PC, vp, vp, vp, vp, i32, vp, vp]
+    lib.rtp_paged_decode_step.restype = ctypes.c_int
+    lib.rtp_paged_decode_step.argtypes = [D, PC, vp, vp, vp, vp, vp, sz, vp]
+    lib.rtp_paged_decode_step_append.restype = ctypes.c_int
+    lib.rtp_paged_decode_step_append.argtypes = [D, PC, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.rtp_read_device_status.restype = ctypes.c_int
     lib.rtp_read_device_status.argtypes = [vp, vp]
     lib.rtp_last_launch_count.restype = i32

@@ -11,6 +11,7 @@
 #include "../../include/rtp.h"
 #include "rtp_attr_cache.h"
 #include "rtp_decode.cuh"
+#include "rtp_paged.cuh"
 #include "rtp_prefill.cuh"
 
 using namespace rtp;
@@ -537,6 +538,192 @@ int rtp_prefill(const rtp_layer_desc* desc, const uint16_t* q_pre, const uint16_
   prefill_kernel<<<g2, kPfThreads, kPfSmem, st>>>(PP);
   g_launches = 2;
   return cudaGetLastError() == cudaSuccess ? RTP_OK : RTP_ECUDA;
+}
+
+}  // extern "C"
+
+// ---- paged caches
+
+namespace {
+
+AttrCache<4, 64> g_attr_paged;  // paged_decode_kernel<type, append>
+
+inline int page_log2(int page) {
+  for (int lg = 4; lg <= 8; ++lg)
+    if (page == (1 << lg)) return lg;
+  return -1;
+}
+
+int check_paged(const rtp_paged_cache* c, int Hkv, PagedPtrs& C) {
+  if (!c || !c->k || !c->v) return RTP_EINVAL;
+  if (c->kv_type != RTP_KV_BF16 && c->kv_type != RTP_KV_E4M3) return RTP_EINVAL;
+  if (!al16(c->k) || !al16(c->v)) return RTP_EINVAL;
+  if (c->kv_type == RTP_KV_E4M3 &&
+      (!c->k_scale || !c->v_scale || !al16(c->k_scale) || !al16(c->v_scale)))
+    return RTP_EINVAL;
+  const int lg = page_log2(c->page_size);
+  if (lg < 0 || c->n_pages < 1) return RTP_ESHAPE;
+  if (((int64_t)c->n_pages << lg) > 0x7fffffffLL) return RTP_ESHAPE;    // slots are int32
+  const int64_t block = (int64_t)Hkv << lg;
+  if (c->page_stride != 0 && c->page_stride < block) return RTP_ESHAPE;
+  C.k = static_cast<unsigned char*>(c->k);
+  C.v = static_cast<unsigned char*>(c->v);
+  C.ks = c->k_scale;
+  C.vs = c->v_scale;
+  C.table = c->block_table;
+  C.page_stride = c->page_stride ? c->page_stride : block;
+  C.table_stride = c->table_stride;
+  C.n_pages = c->n_pages;
+  C.lg = lg;
+  return RTP_OK;
+}
+
+template <int KV, bool APPEND>
+int launch_paged(const PagedDecodeParams& P, const DevInfo& di, cudaStream_t st) {
+  constexpr int smem = PagedSmem<KV>::kBytes;
+  const int rc = g_attr_paged.ensure(2 * KV + (APPEND ? 1 : 0), di.dev, smem, [](int, int bytes) {
+    return cudaFuncSetAttribute(paged_decode_kernel<KV, APPEND>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess
+               ? 0 : 1;
+  });
+  if (rc != 0) return RTP_ECUDA;
+  constexpr int nw = PagedCfg<KV>::kWarps;
+  // no more CTAs than the longest lengths could give a tile per warp
+  const int64_t most = (int64_t)P.L.B * P.L.Hkv * ((P.L.maxN + 15) / 16);
+  const int grid = (int)std::min<int64_t>(std::min(di.sms, kPagedMaxCTAs), (most + nw - 1) / nw);
+  paged_decode_kernel<KV, APPEND><<<grid, nw * 32, smem, st>>>(P);
+  g_launches = 1;
+  return cudaGetLastError() == cudaSuccess ? RTP_OK : RTP_ECUDA;
+}
+
+// rtp_paged_decode_step, with the decode token's append in the launch where append is set
+int paged_decode_impl(const rtp_layer_desc* desc, const rtp_paged_cache* cache,
+                      const uint16_t* k_new, const uint16_t* v_new, bool append,
+                      const uint16_t* q_pre, const int32_t* seq_lens, uint16_t* out, float* lse,
+                      void* ws, size_t ws_bytes, rtp_stream_t stream) {
+  g_launches = 0;
+  if (const int inj = take_injected()) return inj;
+  PagedDecodeParams P;
+  int rc = check_desc(desc, P.L);
+  if (rc != RTP_OK) return rc;
+  rc = check_paged(cache, P.L.Hkv, P.C);
+  if (rc != RTP_OK) return rc;
+  if (!P.C.table || !q_pre || !seq_lens || !out || (append && (!k_new || !v_new)))
+    return RTP_EINVAL;
+  if (P.C.table_stride < 1) return RTP_ESHAPE;
+  if (!al16(q_pre) || !al16(out) || !al16(k_new) || !al16(v_new)) return RTP_EINVAL;
+  if (!ws || ws_bytes < rtp_paged_workspace_bytes(desc)) return RTP_EWORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(ws) & 255) != 0) return RTP_EWORKSPACE;
+  DevInfo di;
+  if (dev_info(di) != RTP_OK) return RTP_ECUDA;
+  P.q_pre = q_pre; P.k_new = k_new; P.v_new = v_new;
+  P.seq_lens = seq_lens; P.out = out; P.lse = lse;
+  P.status = static_cast<int*>(ws);
+  P.arrive = at<uint32_t>(ws, 256);
+  P.part = at<float>(ws, kPagedCtrlBytes);
+  cudaStream_t st = (cudaStream_t)stream;
+  if (cache->kv_type == RTP_KV_BF16)
+    return append ? launch_paged<kKvBf16, true>(P, di, st) : launch_paged<kKvBf16, false>(P, di, st);
+  return append ? launch_paged<kKvE4m3, true>(P, di, st) : launch_paged<kKvE4m3, false>(P, di, st);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t rtp_paged_workspace_bytes(const rtp_layer_desc* desc) {
+  LayerShape L;
+  if (check_desc(desc, L) != RTP_OK) return 0;
+  return RTP_PAGED_CTRL_BYTES +
+         size_t(2) * kPagedMaxCTAs * part_gmem_floats(L.G) * sizeof(float);
+}
+
+int rtp_paged_workspace_init(void* ws, size_t ws_bytes, rtp_stream_t stream) {
+  if (!ws || ws_bytes < RTP_PAGED_CTRL_BYTES) return RTP_EWORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(ws) & 255) != 0) return RTP_EWORKSPACE;
+  return cudaMemsetAsync(ws, 0, RTP_PAGED_CTRL_BYTES, (cudaStream_t)stream) == cudaSuccess
+             ? RTP_OK : RTP_ECUDA;
+}
+
+int rtp_paged_reserve(const rtp_page_pool* pool, const int32_t* lens, const int32_t* new_lens,
+                      const int64_t* counters, int32_t* lens_out, int64_t* counters_out,
+                      int32_t* slot_map, int32_t n_new, void* ws, size_t ws_bytes,
+                      rtp_stream_t stream) {
+  g_launches = 0;
+  if (const int inj = take_injected()) return inj;
+  if (!pool || !pool->free_pages || !pool->block_table || !lens || !new_lens || !counters ||
+      !lens_out || !counters_out || n_new < 0 || (n_new > 0 && !slot_map))
+    return RTP_EINVAL;
+  const int lg = page_log2(pool->page_size);
+  if (lg < 0 || pool->B < 1 || pool->B > 4096 || pool->n_pages < 1 || pool->table_stride < 1)
+    return RTP_ESHAPE;
+  if (((int64_t)pool->n_pages << lg) > 0x7fffffffLL) return RTP_ESHAPE;
+  if (!ws || ws_bytes < RTP_PAGED_CTRL_BYTES) return RTP_EWORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(ws) & 255) != 0) return RTP_EWORKSPACE;
+  DevInfo di;
+  if (dev_info(di) != RTP_OK) return RTP_ECUDA;
+  PagedReserveParams P;
+  P.free_pages = pool->free_pages; P.table = pool->block_table; P.slot_map = slot_map;
+  P.lens_out = lens_out; P.lens = lens; P.new_lens = new_lens;
+  P.counters = counters; P.counters_out = counters_out;
+  P.cap = std::min<int64_t>((int64_t)pool->table_stride << lg, 0x7fffffffLL);
+  P.B = pool->B; P.n_new = n_new; P.n_pages = pool->n_pages; P.stride = pool->table_stride;
+  P.lg = lg;
+  P.chunks = std::max({1, (n_new + kResTok - 1) / kResTok,
+                       (pool->table_stride + kResPages - 1) / kResPages});
+  P.status = static_cast<int*>(ws);
+  P.arrive = at<uint32_t>(ws, 4 * kPagedReserveCounter);
+  // about four items a warp, at most one CTA per SM
+  const int64_t items = (int64_t)P.B * P.chunks;
+  const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(di.sms, items / (4 * kResThreads / 32)));
+  paged_reserve_kernel<<<grid, kResThreads, 8 * (size_t)P.B, (cudaStream_t)stream>>>(P);
+  g_launches = 1;
+  return cudaGetLastError() == cudaSuccess ? RTP_OK : RTP_ECUDA;
+}
+
+int rtp_paged_append_kv(const rtp_layer_desc* desc, const rtp_paged_cache* cache,
+                        const uint16_t* k_pre, const uint16_t* v, const int32_t* start_pos,
+                        const int32_t* slot_map, int32_t n_new, void* ws, rtp_stream_t stream) {
+  g_launches = 0;
+  if (const int inj = take_injected()) return inj;
+  LayerShape L;
+  int rc = check_desc(desc, L);
+  if (rc != RTP_OK) return rc;
+  PagedAppendParams P;
+  rc = check_paged(cache, L.Hkv, P.C);
+  if (rc != RTP_OK) return rc;
+  if (!k_pre || !v || !start_pos || !slot_map || n_new < 0) return RTP_EINVAL;
+  if (!al16(k_pre) || !al16(v)) return RTP_EINVAL;
+  if (n_new == 0) return RTP_OK;
+  P.k_pre = k_pre; P.v = v; P.start_pos = start_pos; P.slot_map = slot_map;
+  P.n_new = n_new; P.n_tok = (int64_t)L.B * n_new;
+  P.cap_rows = (int64_t)P.C.n_pages << P.C.lg;
+  P.Hkv = L.Hkv;
+  P.status = static_cast<int*>(ws);
+  memcpy(P.theta, L.theta, sizeof(P.theta));
+  const int64_t grid = (P.n_tok + kPagedAppendTok - 1) / kPagedAppendTok;
+  if (grid > 0x7fffffffLL) return RTP_ESHAPE;
+  if (cache->kv_type == RTP_KV_BF16)
+    paged_append_kernel<kKvBf16><<<(unsigned)grid, 256, 0, (cudaStream_t)stream>>>(P);
+  else
+    paged_append_kernel<kKvE4m3><<<(unsigned)grid, 256, 0, (cudaStream_t)stream>>>(P);
+  g_launches = 1;
+  return cudaGetLastError() == cudaSuccess ? RTP_OK : RTP_ECUDA;
+}
+
+int rtp_paged_decode_step(const rtp_layer_desc* desc, const rtp_paged_cache* cache,
+                          const uint16_t* q_pre, const int32_t* seq_lens, uint16_t* out,
+                          float* lse, void* ws, size_t ws_bytes, rtp_stream_t stream) {
+  return paged_decode_impl(desc, cache, nullptr, nullptr, false, q_pre, seq_lens, out, lse, ws,
+                           ws_bytes, stream);
+}
+
+int rtp_paged_decode_step_append(const rtp_layer_desc* desc, const rtp_paged_cache* cache,
+                                 const uint16_t* k_new, const uint16_t* v_new,
+                                 const uint16_t* q_pre, const int32_t* seq_lens, uint16_t* out,
+                                 float* lse, void* ws, size_t ws_bytes, rtp_stream_t stream) {
+  return paged_decode_impl(desc, cache, k_new, v_new, true, q_pre, seq_lens, out, lse, ws,
+                           ws_bytes, stream);
 }
 
 int rtp_read_device_status(void* ws, rtp_stream_t stream) {

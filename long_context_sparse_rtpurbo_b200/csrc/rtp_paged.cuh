@@ -1,0 +1,1264 @@
+// Decode step of one layer over a paged cache: the G query heads of a KV head attend to the
+// rows of a sequence's pages, every position for retrieval heads, the sinks and the window for
+// local heads:
+//   z_n = R(m) q . k_n / sqrt(128),  o = sum_n softmax(z)_n v_n,  lse = log sum_n exp(z_n).
+//
+// Bound by HBM: 512 B (bf16) or 264 B (e4m3 rows and their scales) per attended row against
+// 4 * 128 * G flops. So the rows are read once for the G heads, through per-warp rings of
+// asynchronous copies, and the arithmetic on them stays in one warp's registers.
+//
+// Work split: a group is a (sequence, KV head) pair, a tile 16 rows. The tiles of all groups
+// form one line, cut into equal ranges for the CTAs and again for their warps, whatever the
+// lengths are. A warp runs its range as one pipeline across group borders; groups that lie
+// inside its range are written straight out. What remains open at a warp's two ends is merged
+// in shared memory, and what remains open at a CTA's two ends goes to the workspace, where the
+// CTA that arrives last at a group merges its parts in the order of the line (no waits, and the
+// result does not depend on who is last).
+#pragma once
+
+#include "rtp_attend.cuh"
+#include "rtp_append.cuh"
+
+namespace rtp {
+
+constexpr int kKvBf16 = 0, kKvE4m3 = 1;
+constexpr int kPagedMaxCTAs = 160;
+constexpr int kPagedCtrlBytes = 4096;       // status word at 0, arrival counters from 256
+constexpr int kPagedReserveCounter = 960;   // word index of the reservation's arrival counter
+constexpr float kE4m3Max = 448.f;
+constexpr float kScaleMin = 1.17549435e-38f;   // 2^-126
+
+struct PagedPtrs {
+  unsigned char *k, *v;          // [n_pages] pages of [Hkv][page][128], page_stride rows apart
+  float *ks, *vs;                // e4m3: [n_pages][Hkv][page]
+  const int32_t* table;          // [B][table_stride]
+  int64_t page_stride;           // rows
+  int table_stride, n_pages, lg; // page = 1 << lg
+};
+
+struct PagedDecodeParams {
+  LayerShape L;
+  PagedPtrs C;
+  const uint16_t *q_pre, *k_new, *v_new;
+  const int32_t* seq_lens;
+  uint16_t* out;
+  float* lse;
+  int* status;
+  uint32_t* arrive;
+  float* part;
+};
+
+template <int KV> struct PagedCfg;
+// 8 warps with three 8 KB tiles each: 192 KB of copies in the ring
+template <> struct PagedCfg<kKvBf16> {
+  static constexpr int kWarps = 8, kStages = 3, kRowB = 256, kTerms = 3;
+  static constexpr int kStageB = 16 * 512;
+};
+template <> struct PagedCfg<kKvE4m3> {
+  static constexpr int kWarps = 8, kStages = 5, kRowB = 128, kTerms = 2;
+  static constexpr int kStageB = 16 * 256 + 128;
+};
+
+// floats of a partial in shared memory (rows of 132: the accumulators' lanes hit all banks) and
+// in the workspace
+constexpr int kPartPitch = 132;
+__host__ __device__ constexpr int part_smem_floats(int G) { return G * kPartPitch + 32; }
+__host__ __device__ constexpr int part_gmem_floats(int G) { return G * kD + 32; }
+
+struct PagedEntry {              // an open end of a warp's range
+  long long gs, ge;              // tiles of its group
+  int gid;                       // sequence * Hkv + position of the KV head in the group order; -1: none
+  int pad;
+};
+
+template <int KV>
+struct PagedSmem {
+  using Cfg = PagedCfg<KV>;
+  static constexpr int kRing = Cfg::kWarps * Cfg::kStages * Cfg::kStageB;
+  static constexpr int kAng = kRing;                               // [warps][64] (cos, sin)
+  static constexpr int kMask = kAng + Cfg::kWarps * 64 * 8;        // [warps][8] row masks
+  static constexpr int kEnt = kMask + Cfg::kWarps * 8 * 4;
+  static constexpr int kPrefix = kEnt + Cfg::kWarps * 2 * (int)sizeof(PagedEntry);
+  static constexpr int kMisc = kPrefix + 130 * 8;
+  static constexpr int kWt = kMisc + 256;                          // [160][8] weights of a merge
+  static constexpr int kBytes = kWt + kPagedMaxCTAs * 8 * 4;
+};
+
+// ------------------------------------------------------------------ conversions and products
+
+__device__ __forceinline__ uint32_t pack_h2(float x, float y) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
+  return r;
+}
+// (x, y) = hi + lo in fp16
+__device__ __forceinline__ void split_h2(float x, float y, uint32_t& hi, uint32_t& lo) {
+  hi = pack_h2(x, y);
+  const __half2 h = *reinterpret_cast<const __half2*>(&hi);
+  lo = pack_h2(x - __low2float(h), y - __high2float(h));
+}
+// two e4m3 bytes -> fp16x2, exact
+__device__ __forceinline__ uint32_t e4m3x2_h2(uint32_t w) {
+  uint32_t r;
+  asm("{.reg .b16 t; cvt.u16.u32 t, %1; cvt.rn.f16x2.e4m3x2 %0, t;}" : "=r"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3x2_h2_hi(uint32_t w) {
+  uint32_t r;
+  asm("{.reg .b16 a, b; mov.b32 {a, b}, %1; cvt.rn.f16x2.e4m3x2 %0, b;}" : "=r"(r) : "r"(w));
+  return r;
+}
+// float -> e4m3, nearest even, values beyond +-448 to +-448
+__device__ __forceinline__ uint32_t f_e4m3x2(float x, float y) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(y), "f"(x));
+  return r;
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// 16-byte copy that writes zeros where n = 0 (the address is not read then)
+__device__ __forceinline__ void cp_async16_zf(uint32_t saddr, const void* gmem, uint32_t n) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(saddr), "l"(gmem), "r"(n)
+               : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float r;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// 2^(a - b), 0 where a is the empty state's -inf
+__device__ __forceinline__ float ex2_from(float a, float b) { return a == -INFINITY ? 0.f : ex2(a - b); }
+__device__ __forceinline__ uint32_t low_mask(int n) { return (1u << min(max(n, 0), 16)) - 1u; }
+
+// The stored scale of a row: amax / 448 in single precision, at least 2^-126 (a zero row).
+__device__ __forceinline__ float row_scale(float amax) {
+  return fmaxf(__fdiv_rn(amax, kE4m3Max), kScaleMin);
+}
+
+// ------------------------------------------------------------------ the line of tiles
+
+// Length of sequence b; 0 (no tiles) for an empty or an invalid one.
+__device__ __forceinline__ int paged_len(const PagedDecodeParams& P, int b, bool* bad) {
+  if (b >= P.L.B) return 0;
+  const int n = P.seq_lens[b];
+  const int64_t cap = min((int64_t)P.C.table_stride << P.C.lg, P.L.maxN);
+  if (n < 0 || n > cap) { if (bad) *bad = true; return 0; }
+  return n;
+}
+
+// Tiles of a local head: those of the sinks, then those of the window that come after them.
+struct LocalTiles { int ns, sh, lo, nt; };
+__device__ __forceinline__ LocalTiles local_tiles(const LayerShape& L, int n) {
+  LocalTiles t;
+  const int tr = (n + 15) >> 4;
+  t.ns = min((int)(((int64_t)L.sinks + 15) >> 4), tr);
+  t.lo = max(0, n - L.window);
+  const int wt = max(t.ns, t.lo >> 4);
+  t.sh = wt - t.ns;
+  t.nt = t.ns + tr - wt;
+  return t;
+}
+__device__ __forceinline__ long long seq_tiles(const LayerShape& L, int n) {
+  if (n <= 0) return 0;
+  return (long long)L.n_ret * ((n + 15) >> 4) + (long long)L.n_loc * local_tiles(L, n).nt;
+}
+
+// A place on the line. Sequences are in batch order; in a sequence the retrieval KV heads come
+// first. lens: this lane's length of the 32 sequences around b.
+struct Cursor {
+  int b, gi, k, nt, n, lens;
+  int ns, sh, lo;                // tile k covers rows from 16 (k < ns ? k : k + sh); window from lo
+};
+
+__device__ __forceinline__ int kv_head(const LayerShape& L, int gi) {
+  return gi < L.n_ret ? L.ret_kv[gi] : L.loc_kv[gi - L.n_ret];
+}
+__device__ __forceinline__ void cursor_group(const LayerShape& L, Cursor& c) {
+  if (c.gi < L.n_ret) {
+    c.ns = 0; c.sh = 0; c.lo = 0; c.nt = (c.n + 15) >> 4;
+  } else {
+    const LocalTiles t = local_tiles(L, c.n);
+    c.ns = t.ns; c.sh = t.sh; c.lo = t.lo; c.nt = t.nt;
+  }
+}
+__device__ __forceinline__ void cursor_next_group(const PagedDecodeParams& P, Cursor& c) {
+  c.k = 0;
+  if (++c.gi == P.L.Hkv) {
+    c.gi = 0;
+    do {
+      ++c.b;
+      if ((c.b & 31) == 0) c.lens = paged_len(P, c.b + (threadIdx.x & 31), nullptr);
+      c.n = __shfl_sync(0xffffffffu, c.lens, c.b & 31);
+    } while (c.n == 0 && c.b < P.L.B);
+  }
+  cursor_group(P.L, c);
+}
+// The cursor of tile t (< the number of tiles); prefix: tiles before each 32 sequences.
+__device__ __forceinline__ Cursor cursor_at(const PagedDecodeParams& P, const long long* prefix,
+                                            long long t) {
+  const int lane = threadIdx.x & 31, nc = (P.L.B + 31) >> 5;
+  int before = 0;                              // chunks that start at or before t
+  for (int i = lane; i < nc; i += 32) before += prefix[i] <= t;
+  before = __reduce_add_sync(0xffffffffu, before);
+  Cursor c;
+  const int chunk = before - 1;
+  c.lens = paged_len(P, chunk * 32 + lane, nullptr);
+  const long long mine = seq_tiles(P.L, c.lens);
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += u;
+  }
+  const long long rel = t - prefix[chunk];
+  const int j = __popc(__ballot_sync(0xffffffffu, incl <= rel));
+  c.b = chunk * 32 + j;
+  c.n = __shfl_sync(0xffffffffu, c.lens, j);
+  const int in_seq = (int)(rel - __shfl_sync(0xffffffffu, incl - mine, j));
+  const int tr = (c.n + 15) >> 4;
+  if (in_seq < P.L.n_ret * tr) {
+    c.gi = in_seq / tr;
+    c.k = in_seq - c.gi * tr;
+  } else {
+    const int u = in_seq - P.L.n_ret * tr, tl = local_tiles(P.L, c.n).nt;
+    c.gi = P.L.n_ret + u / tl;
+    c.k = u % tl;
+  }
+  cursor_group(P.L, c);
+  return c;
+}
+
+struct TileDesc { int pid, row; uint32_t mask; };   // page, row in the page block, rows attended
+__device__ __forceinline__ TileDesc tile_desc(const PagedDecodeParams& P, const Cursor& c) {
+  const int pos = 16 * (c.k < c.ns ? c.k : c.k + c.sh);
+  TileDesc d;
+  d.pid = __ldg(P.C.table + (int64_t)c.b * P.C.table_stride + (pos >> P.C.lg));
+  d.row = (kv_head(P.L, c.gi) << P.C.lg) + (pos & ((1 << P.C.lg) - 1));
+  d.mask = low_mask(c.n - pos) & (low_mask(P.L.sinks - pos) | ~low_mask(c.lo - pos));
+  return d;
+}
+
+// Starts the copies of a tile into a stage of this warp's ring; *mask_slot gets its row mask.
+// Rows that are not attended become zeros, so that what a page holds there (NaN included) takes
+// no part. Each copy instruction moves 512 contiguous bytes; 16-byte chunks are XOR-swizzled by
+// the row, so that the ldmatrix reads of eight rows hit all banks.
+template <int KV>
+__device__ __forceinline__ void tile_issue(const PagedDecodeParams& P, const TileDesc& d,
+                                           uint32_t stage, uint32_t* mask_slot) {
+  using Cfg = PagedCfg<KV>;
+  const int lane = threadIdx.x & 31;
+  uint32_t mask = d.mask;
+  int64_t pid = d.pid;
+  if ((uint32_t)d.pid >= (uint32_t)P.C.n_pages) {      // a page that does not exist: no rows
+    if (lane == 0) set_status(P.status, -6);
+    mask = 0;
+    pid = 0;
+  }
+  if (lane == 0) *mask_slot = mask;
+  const int64_t off = (pid * P.C.page_stride + d.row) * Cfg::kRowB + lane * 16;
+  const unsigned char* kp = P.C.k + off;
+  const unsigned char* vp = P.C.v + off;
+  constexpr int kCh = Cfg::kRowB / 16;                 // chunks per row: 16 or 8
+  const int r0 = lane / kCh, c0 = lane % kCh;          // rows of one instruction: 2 or 4
+  constexpr int kRows = 32 / kCh;
+  const uint32_t dst = stage + r0 * Cfg::kRowB;
+  const uint32_t sw = (uint32_t)(c0 ^ r0) << 4;
+  if (mask == 0xffffu) {
+#pragma unroll
+    for (int u = 0; u < 16 / kRows; ++u) {
+      const uint32_t s = dst + u * 512 + (sw ^ (uint32_t)(((u * kRows) & 7) << 4));
+      cp_async16_s(s, kp + u * 512);
+      cp_async16_s(s + 16 * Cfg::kRowB, vp + u * 512);
+    }
+  } else {
+#pragma unroll
+    for (int u = 0; u < 16 / kRows; ++u) {
+      const uint32_t s = dst + u * 512 + (sw ^ (uint32_t)(((u * kRows) & 7) << 4));
+      const uint32_t n = (mask >> (u * kRows + r0)) & 1u ? 16u : 0u;
+      cp_async16_zf(s, kp + u * 512, n);
+      cp_async16_zf(s + 16 * Cfg::kRowB, vp + u * 512, n);
+    }
+  }
+  if (KV == kKvE4m3 && lane < 8) {                     // 16 scales of K, then of V
+    const float* sp = (lane < 4 ? P.C.ks : P.C.vs) +
+                      pid * ((int64_t)P.L.Hkv << P.C.lg) + d.row + (lane & 3) * 4;
+    cp_async16_s(stage + 32 * Cfg::kRowB + lane * 16, sp);
+  }
+}
+
+// ------------------------------------------------------------------ one warp's attention
+
+// Softmax state of a group's heads 2t and 2t + 1 (t = lane % 4) and the O^T accumulators. The
+// weights of the sum l are 2^(z - m). Those of the accumulators are 2^(z + log2(v scale) - mo),
+// with mo = m in a bf16 cache: the references are separate because rows carry their own scale.
+template <int KV>
+struct PagedAttn {
+  float acc[8][4];
+  float m[2], l[2], mo[2];
+  uint32_t q[8][2 * PagedCfg<KV>::kTerms];     // B fragments of Q^T, one pair per term
+  float qf[2];                                 // e4m3: power of two taken out of the heads' query
+};
+
+template <int KV>
+__device__ __forceinline__ void attn_reset(PagedAttn<KV>& A) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) A.acc[i][e] = 0.f;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) { A.m[e] = -INFINITY; A.mo[e] = -INFINITY; A.l[e] = 0.f; }
+}
+
+// (cos, sin) of the query position's 64 angles into this warp's table
+__device__ __forceinline__ void fill_angles(const LayerShape& L, float2* ang, int pos) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    float s, c;
+    rope_sincosf((double)pos, L.theta[lane + 32 * e], &s, &c);
+    ang[lane + 32 * e] = make_float2(c, s);
+  }
+  __syncwarp();
+}
+
+// R(m) q log2(e) / sqrt(128) of the G heads as B fragments. bf16 cache: three bf16 terms (24
+// bits). e4m3 cache: two fp16 terms (22 bits) of the query divided by a power of two that
+// brings its largest element into [1, 2), since fp16 has few exponents.
+template <int KV>
+__device__ __forceinline__ void load_query(const PagedDecodeParams& P, PagedAttn<KV>& A, int b,
+                                           int g, const float2* ang) {
+  const int lane = threadIdx.x & 31, h = lane >> 2, t = lane & 3;
+  const int G = P.L.G;
+  const float sc = kLog2e * 0.08838834764831845f;      // 1 / sqrt(128)
+  const uint16_t* q = P.q_pre + ((int64_t)b * P.L.Hq + (int64_t)g * G + min(h, G - 1)) * kD;
+  float x[8][4];
+#pragma unroll
+  for (int kk = 0; kk < 4; ++kk) {
+    // channels c..c+1 and c2..c2+1 of this lane in the step's first and second half
+    const int c = KV == kKvBf16 ? 16 * kk + 2 * t : 16 * kk + 4 * t;
+    const int c2 = KV == kKvBf16 ? c + 8 : c + 2;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int i = e ? c2 : c;
+      const uint32_t lo = *reinterpret_cast<const uint32_t*>(q + i);
+      const uint32_t hi = *reinterpret_cast<const uint32_t*>(q + i + 64);
+      const float4 a = *reinterpret_cast<const float4*>(ang + i);
+      x[kk][2 * e] = (bf_lo(lo) * a.x - bf_lo(hi) * a.y) * sc;
+      x[kk][2 * e + 1] = (bf_hi(lo) * a.z - bf_hi(hi) * a.w) * sc;
+      x[kk + 4][2 * e] = (bf_lo(lo) * a.y + bf_lo(hi) * a.x) * sc;
+      x[kk + 4][2 * e + 1] = (bf_hi(lo) * a.w + bf_hi(hi) * a.z) * sc;
+    }
+  }
+  if (h >= G) {
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[kk][e] = 0.f;
+  }
+  if (KV == kKvE4m3) {
+    float mx = 0.f;
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) mx = fmaxf(mx, fabsf(x[kk][e]));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    const int ex = min(max((int)(__float_as_uint(mx) >> 23), 1), 253);
+    const float down = __uint_as_float((uint32_t)(254 - ex) << 23);
+    const float up = __uint_as_float((uint32_t)ex << 23);
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        split_h2(x[kk][2 * e] * down, x[kk][2 * e + 1] * down, A.q[kk][e], A.q[kk][2 + e]);
+    A.qf[0] = __shfl_sync(0xffffffffu, up, 8 * t);
+    A.qf[1] = __shfl_sync(0xffffffffu, up, 8 * t + 4);
+  } else {
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float a = x[kk][2 * e], b2 = x[kk][2 * e + 1];
+        const uint32_t hi = pack_bf2(a, b2);
+        const float ra = a - bf_lo(hi), rb = b2 - bf_hi(hi);
+        A.q[kk][e] = hi;
+        split_bf2(ra, rb, A.q[kk][2 + e], A.q[kk][(KV == kKvBf16 ? 4 : 0) + e]);
+      }
+  }
+}
+
+// Moves a reference: x holds this lane's logits of the two heads (rows g, g + 8). It only moves
+// when a logit is more than 2^8 above it (the weights then stay below 2^8), so most tiles cost
+// one vote instead of the maximum over the rows.
+__device__ __forceinline__ bool move_ref(const float (&x)[4], float (&m)[2], float (&al)[2]) {
+  const bool up = x[0] > m[0] + 8.f || x[2] > m[0] + 8.f || x[1] > m[1] + 8.f || x[3] > m[1] + 8.f;
+  if (!__any_sync(0xffffffffu, up)) return false;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    float mx = fmaxf(x[e], x[2 + e]);
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    const float mn = fmaxf(m[e], mx);
+    al[e] = mn == -INFINITY ? 1.f : ex2(m[e] - mn);
+    m[e] = mn;
+  }
+  return true;
+}
+
+// One tile of 16 rows. Logits S^T = K Q^T, weights as B operand of O^T += V^T P^T (two terms).
+template <int KV>
+__device__ __forceinline__ void paged_tile(PagedAttn<KV>& A, uint32_t stage, uint32_t mask) {
+  using Cfg = PagedCfg<KV>;
+  const int lane = threadIdx.x & 31, g = lane >> 2;
+  const uint32_t tv = stage + 16 * Cfg::kRowB;
+  float x[4];
+  float vs[2];
+  if (KV == kKvBf16) {
+    float s[3][4];
+#pragma unroll
+    for (int j = 0; j < 3; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[j][e] = 0.f;
+    const int r = lane & 15;
+    const uint32_t ka = stage + r * 256 + (uint32_t)(((lane >> 4) ^ (r & 7)) << 4);
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk) {
+      uint32_t a[4];
+      ldsm_x4(ka ^ (uint32_t)(kk << 5), a);
+#pragma unroll
+      for (int j = 0; j < 3; ++j) mma_bf16(s[j], a, A.q[kk][2 * j], A.q[kk][2 * j + 1]);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = s[0][e] + (s[1][e] + s[2][e]);
+  } else {
+    float s[2][4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[j][e] = 0.f;
+    const int r = lane & 15;
+    const uint32_t ka = stage + r * 128 + (uint32_t)(((lane >> 4) ^ (r & 7)) << 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t w[4];
+      ldsm_x4(ka ^ (uint32_t)(i << 5), w);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const uint32_t a[4] = {e4m3x2_h2(w[2 * c]), e4m3x2_h2(w[2 * c + 1]),
+                               e4m3x2_h2_hi(w[2 * c]), e4m3x2_h2_hi(w[2 * c + 1])};
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          mma_f16(s[j], a, A.q[2 * i + c][2 * j], A.q[2 * i + c][2 * j + 1]);
+      }
+    }
+    const uint32_t sc = stage + 32 * Cfg::kRowB + g * 4;
+    float k0, k1;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(k0) : "r"(sc) : "memory");
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(k1) : "r"(sc + 32) : "memory");
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(vs[0]) : "r"(sc + 64) : "memory");
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(vs[1]) : "r"(sc + 96) : "memory");
+    x[0] = (s[0][0] + s[1][0]) * (k0 * A.qf[0]);
+    x[1] = (s[0][1] + s[1][1]) * (k0 * A.qf[1]);
+    x[2] = (s[0][2] + s[1][2]) * (k1 * A.qf[0]);
+    x[3] = (s[0][3] + s[1][3]) * (k1 * A.qf[1]);
+  }
+  if (!((mask >> g) & 1u)) { x[0] = -INFINITY; x[1] = -INFINITY; }
+  if (!((mask >> (g + 8)) & 1u)) { x[2] = -INFINITY; x[3] = -INFINITY; }
+  float al[2] = {1.f, 1.f};
+  const bool moved = move_ref(x, A.m, al);
+  float p[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) p[e] = ex2_from(x[e], A.m[e & 1]);
+  if (moved) { A.l[0] *= al[0]; A.l[1] *= al[1]; }
+  A.l[0] += p[0] + p[2];
+  A.l[1] += p[1] + p[3];
+  bool moved_o = moved;
+  if (KV == kKvE4m3) {
+    // weights of the rows with their scales, against their own reference
+    const float lv0 = lg2(vs[0]), lv1 = lg2(vs[1]);
+    float y[4];
+    y[0] = (mask >> g) & 1u ? x[0] + lv0 : -INFINITY;
+    y[1] = (mask >> g) & 1u ? x[1] + lv0 : -INFINITY;
+    y[2] = (mask >> (g + 8)) & 1u ? x[2] + lv1 : -INFINITY;
+    y[3] = (mask >> (g + 8)) & 1u ? x[3] + lv1 : -INFINITY;
+    al[0] = al[1] = 1.f;
+    moved_o = move_ref(y, A.mo, al);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) p[e] = ex2_from(y[e], A.mo[e & 1]);
+  } else {
+    A.mo[0] = A.m[0];
+    A.mo[1] = A.m[1];
+  }
+  if (moved_o) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      A.acc[i][0] *= al[0]; A.acc[i][1] *= al[1];
+      A.acc[i][2] *= al[0]; A.acc[i][3] *= al[1];
+    }
+  }
+  uint32_t h01, l01, h23, l23;
+  if (KV == kKvBf16) {
+    split_bf2(p[0], p[1], h01, l01);
+    split_bf2(p[2], p[3], h23, l23);
+  } else {
+    split_h2(p[0], p[1], h01, l01);
+    split_h2(p[2], p[3], h23, l23);
+  }
+  const uint32_t bh0 = movm_t(h01), bh1 = movm_t(h23);
+  const uint32_t bl0 = movm_t(l01), bl1 = movm_t(l23);
+  if (KV == kKvBf16) {
+    const int j = lane >> 3, r = (lane & 7) + (j >> 1) * 8;
+    const uint32_t va = tv + r * 256 + (uint32_t)(((j & 1) ^ (lane & 7)) << 4);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint32_t a[4];
+      ldsm_x4_t(va ^ (uint32_t)(i << 5), a);
+      mma_bf16(A.acc[i], a, bh0, bh1);
+      mma_bf16(A.acc[i], a, bl0, bl1);
+    }
+  } else {
+    // a transposed 16-bit element is a pair of channels (2 g, 2 g + 1) of one token: row g of
+    // the product takes the even channel, row g + 8 the odd one
+    const int r = lane & 15;
+    const uint32_t va = tv + r * 128 + (uint32_t)(((lane >> 4) ^ (r & 7)) << 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t w[4];
+      ldsm_x4_t(va ^ (uint32_t)(i << 5), w);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const uint32_t u0 = __byte_perm(w[2 * c], 0, 0x3120), u1 = __byte_perm(w[2 * c + 1], 0, 0x3120);
+        const uint32_t a[4] = {e4m3x2_h2(u0), e4m3x2_h2_hi(u0), e4m3x2_h2(u1), e4m3x2_h2_hi(u1)};
+        mma_f16(A.acc[2 * i + c], a, bh0, bh1);
+        mma_f16(A.acc[2 * i + c], a, bl0, bl1);
+      }
+    }
+  }
+}
+
+// Channel of accumulator element e (0..3) of 16-channel block i in this lane
+template <int KV>
+__device__ __forceinline__ int acc_channel(int i, int e) {
+  const int g = (threadIdx.x & 31) >> 2;
+  return KV == kKvBf16 ? 16 * i + g + 8 * (e >> 1) : 16 * i + 2 * g + (e >> 1);
+}
+
+// The sum over the rows of each head (a lane has those of rows g and g + 8 of every tile)
+template <int KV>
+__device__ __forceinline__ void attn_sum(PagedAttn<KV>& A) {
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) A.l[e] += __shfl_xor_sync(0xffffffffu, A.l[e], o);
+}
+
+// Output rows of a group that this warp holds whole
+template <int KV>
+__device__ __forceinline__ void attn_write(const PagedDecodeParams& P, const PagedAttn<KV>& A,
+                                           int b, int g) {
+  const int lane = threadIdx.x & 31, t = lane & 3, gr = lane >> 2, G = P.L.G;
+  const int64_t head0 = (int64_t)b * P.L.Hq + (int64_t)g * G;
+  float f[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+    f[e] = A.l[e] > 0.f || A.l[e] != A.l[e] ? ex2_from(A.mo[e], A.m[e]) / A.l[e] : 0.f;
+  if (P.lse && gr == 0) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      if (2 * t + e < G) P.lse[head0 + 2 * t + e] = (A.m[e] + log2f(A.l[e])) * 0.6931471805599453f;
+  }
+  if (KV == kKvBf16) {
+    // transposed in registers: a lane then has two neighbouring channels of head gr
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t w = movm_t(pack_bf2(A.acc[i][2 * u] * f[0], A.acc[i][2 * u + 1] * f[1]));
+        if (gr < G)
+          *reinterpret_cast<uint32_t*>(P.out + (head0 + gr) * kD + 16 * i + 8 * u + 2 * t) = w;
+      }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (2 * t + e < G)
+          *reinterpret_cast<uint32_t*>(P.out + (head0 + 2 * t + e) * kD + 16 * i + 2 * gr) =
+              pack_bf2(A.acc[i][e] * f[e], A.acc[i][2 + e] * f[e]);
+  }
+}
+
+// A partial in shared memory: [G][132] accumulators, then (m, l, mo) per head
+template <int KV>
+__device__ __forceinline__ void attn_store(const PagedAttn<KV>& A, float* dst, int G) {
+  const int lane = threadIdx.x & 31, t = lane & 3;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int h = 2 * t + e;
+    if (h < G) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        dst[h * kPartPitch + acc_channel<KV>(i, e)] = A.acc[i][e];
+        dst[h * kPartPitch + acc_channel<KV>(i, 2 + e)] = A.acc[i][2 + e];
+      }
+      if ((lane >> 2) == 0) {
+        float* ml = dst + G * kPartPitch + 3 * h;
+        ml[0] = A.m[e]; ml[1] = A.l[e]; ml[2] = A.mo[e];
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ the new token's row
+
+// Writes the decode token's key and value of KV head g at its page row and into its row of the
+// staged tile (one warp). The rotation and the roundings are those of the bulk append.
+template <int KV>
+__device__ __noinline__ void paged_append_row(const PagedDecodeParams& P, int b, int g, int pos,
+                                              int64_t row, int64_t srow, uint32_t stage) {
+  using Cfg = PagedCfg<KV>;
+  const int lane = threadIdx.x & 31, r = pos & 15;
+  const uint16_t* kp = P.k_new + ((int64_t)b * P.L.Hkv + g) * kD;
+  const uint16_t* vp = P.v_new + ((int64_t)b * P.L.Hkv + g) * kD;
+  const uint32_t kt = stage + r * Cfg::kRowB, vt = kt + 16 * Cfg::kRowB;
+  unsigned char* kd = P.C.k + row * Cfg::kRowB;
+  unsigned char* vd = P.C.v + row * Cfg::kRowB;
+  // lane: channels 2 lane, 2 lane + 1 and their partners 64 on
+  const uint32_t a = *reinterpret_cast<const uint32_t*>(kp + 2 * lane);
+  const uint32_t c = *reinterpret_cast<const uint32_t*>(kp + 64 + 2 * lane);
+  const uint32_t va = *reinterpret_cast<const uint32_t*>(vp + 2 * lane);
+  const uint32_t vc = *reinterpret_cast<const uint32_t*>(vp + 64 + 2 * lane);
+  double lo[2], hi[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    double sn, cs;
+    rope_sincos((double)pos, P.L.theta[2 * lane + e], &sn, &cs);
+    const double xa = e ? bf_hi(a) : bf_lo(a), xb = e ? bf_hi(c) : bf_lo(c);
+    lo[e] = xa * cs - xb * sn;
+    hi[e] = xa * sn + xb * cs;
+  }
+  const uint32_t sw = (uint32_t)(r & 7) << 4;
+  if (KV == kKvBf16) {
+    const uint32_t kl = d2bf_rn(lo[0]) | (uint32_t)d2bf_rn(lo[1]) << 16;
+    const uint32_t kh = d2bf_rn(hi[0]) | (uint32_t)d2bf_rn(hi[1]) << 16;
+    *reinterpret_cast<uint32_t*>(kd + 4 * lane) = kl;
+    *reinterpret_cast<uint32_t*>(kd + 128 + 4 * lane) = kh;
+    *reinterpret_cast<uint32_t*>(vd + 4 * lane) = va;
+    *reinterpret_cast<uint32_t*>(vd + 128 + 4 * lane) = vc;
+    const uint32_t o = (4u * lane) ^ sw;
+    st_shared_u32(kt + o, kl);
+    st_shared_u32(kt + (o ^ 128u), kh);
+    st_shared_u32(vt + o, va);
+    st_shared_u32(vt + (o ^ 128u), vc);
+  } else {
+    float x[2][4] = {{(float)lo[0], (float)lo[1], (float)hi[0], (float)hi[1]},
+                     {bf_lo(va), bf_hi(va), bf_lo(vc), bf_hi(vc)}};
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      float mx = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) mx = fmaxf(mx, fabsf(x[j][e]));
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      const float sc = row_scale(mx);
+      const uint32_t w0 = f_e4m3x2(__fdiv_rn(x[j][0], sc), __fdiv_rn(x[j][1], sc));
+      const uint32_t w1 = f_e4m3x2(__fdiv_rn(x[j][2], sc), __fdiv_rn(x[j][3], sc));
+      unsigned char* d = j ? vd : kd;
+      *reinterpret_cast<uint16_t*>(d + 2 * lane) = (uint16_t)w0;
+      *reinterpret_cast<uint16_t*>(d + 64 + 2 * lane) = (uint16_t)w1;
+      const uint32_t o = (2u * lane) ^ sw;
+      const uint32_t tb = j ? vt : kt;
+      asm volatile("st.shared.u16 [%0], %1;" ::"r"(tb + o), "h"((uint16_t)w0) : "memory");
+      asm volatile("st.shared.u16 [%0], %1;" ::"r"(tb + (o ^ 64u)), "h"((uint16_t)w1) : "memory");
+      if (lane == 0) {
+        (j ? P.C.vs : P.C.ks)[srow] = sc;
+        st_shared_u32(stage + 32 * Cfg::kRowB + 64 * j + 4 * r, __float_as_uint(sc));
+      }
+    }
+  }
+  __syncwarp();
+}
+
+// ------------------------------------------------------------------ the kernel
+
+template <int KV, bool APPEND>
+__global__ void __launch_bounds__(PagedCfg<KV>::kWarps * 32, 1)
+paged_decode_kernel(const __grid_constant__ PagedDecodeParams P) {
+  using Cfg = PagedCfg<KV>;
+  using S = PagedSmem<KV>;
+  constexpr int NW = Cfg::kWarps, NT = NW * 32, NS = Cfg::kStages;
+  extern __shared__ __align__(1024) unsigned char sm[];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const LayerShape& L = P.L;
+  const int G = L.G;
+  long long* prefix = reinterpret_cast<long long*>(sm + S::kPrefix);
+  PagedEntry* ent = reinterpret_cast<PagedEntry*>(sm + S::kEnt);
+  float2* ang = reinterpret_cast<float2*>(sm + S::kAng) + warp * 64;
+  uint32_t* masks = reinterpret_cast<uint32_t*>(sm + S::kMask) + warp * 8;
+
+  // ---- tiles before each 32 sequences; outputs of sequences that have none
+  const int nc = (L.B + 31) >> 5;
+  for (int ch = warp; ch < nc; ch += NW) {
+    const int b = ch * 32 + lane;
+    bool bad = false;
+    const int n = paged_len(P, b, &bad);
+    if (bad && blockIdx.x == 0) set_status(P.status, -6);
+    long long t = seq_tiles(L, n);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    if (lane == 0) prefix[ch] = t;
+    uint32_t none = __ballot_sync(0xffffffffu, b < L.B && n == 0 && b % gridDim.x == blockIdx.x);
+    while (none) {
+      const int64_t e = ch * 32 + __ffs(none) - 1;
+      none &= none - 1;
+      uint4* o = reinterpret_cast<uint4*>(P.out + e * L.Hq * kD);
+      for (int i = lane; i < L.Hq * (kD / 8); i += 32) o[i] = make_uint4(0, 0, 0, 0);
+      if (P.lse)
+        for (int i = lane; i < L.Hq; i += 32) P.lse[e * L.Hq + i] = -INFINITY;
+    }
+  }
+  if (tid < 2 * NW) ent[tid].gid = -1;
+  __syncthreads();
+  if (warp == 0) {                                     // exclusive sums, the total at [nc]
+    long long run = 0;
+    for (int c0 = 0; c0 < nc; c0 += 32) {
+      const long long mine = c0 + lane < nc ? prefix[c0 + lane] : 0;
+      long long incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += u;
+      }
+      if (c0 + lane < nc) prefix[c0 + lane] = run + incl - mine;
+      run += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) prefix[nc] = run;
+  }
+  __syncthreads();
+  const long long T = prefix[nc];
+  // CTAs that take part: at least one tile per warp
+  const long long PC = min((long long)gridDim.x, (T + NW - 1) / NW);
+  if (blockIdx.x >= PC) return;
+  const long long ct0 = blockIdx.x * T / PC, ct1 = (blockIdx.x + 1) * T / PC;
+  const long long t0 = ct0 + warp * (ct1 - ct0) / NW, t1 = ct0 + (warp + 1) * (ct1 - ct0) / NW;
+  const int n = (int)(t1 - t0);
+
+  unsigned char* ring = sm + warp * NS * Cfg::kStageB;
+  const uint32_t ring_s = smem_u32(ring);
+  PagedAttn<KV> A;
+  if (n > 0) {
+    Cursor cc = cursor_at(P, prefix, t0), pc = cc;
+    // fill the ring: the page ids of its tiles are loaded together
+    TileDesc d[NS];
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      if (s < n) {
+        d[s] = tile_desc(P, pc);
+        if (++pc.k == pc.nt) cursor_next_group(P, pc);
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      if (s < n) tile_issue<KV>(P, d[s], ring_s + s * Cfg::kStageB, masks + s);
+      cp_async_commit();
+    }
+    TileDesc nx;                                       // the next tile, its page id on the way
+    if (NS < n) {
+      nx = tile_desc(P, pc);
+      if (++pc.k == pc.nt) cursor_next_group(P, pc);
+    }
+    int seg_k = cc.k, ang_b = -1, slot = 0;
+    bool have_head = false;
+    PagedEntry he;
+    float sv[8][4], sv_m[2], sv_l[2], sv_mo[2];
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      const int kvh = kv_head(L, cc.gi);
+      if (cc.k == seg_k) {                             // first tile of a group or of the range
+        if (cc.b != ang_b) {
+          fill_angles(L, ang, cc.n - 1);
+          ang_b = cc.b;
+        }
+        load_query<KV>(P, A, cc.b, kvh, ang);
+        attn_reset<KV>(A);
+      }
+      cp_async_wait<NS - 1>();
+      __syncwarp();
+      const uint32_t stage = ring_s + slot * Cfg::kStageB;
+      const uint32_t mask = masks[slot];
+      if (APPEND && cc.k == cc.nt - 1 && mask) {       // the last tile holds the new token's row
+        const int pos = cc.n - 1;
+        const int64_t pid = __ldg(P.C.table + (int64_t)cc.b * P.C.table_stride + (pos >> P.C.lg));
+        const int64_t in = ((int64_t)kvh << P.C.lg) + (pos & ((1 << P.C.lg) - 1));
+        paged_append_row<KV>(P, cc.b, kvh, pos, pid * P.C.page_stride + in,
+                             pid * ((int64_t)L.Hkv << P.C.lg) + in, stage);
+      }
+      paged_tile<KV>(A, stage, mask);
+      __syncwarp();
+      if (i + NS < n) {
+        tile_issue<KV>(P, nx, stage, masks + slot);
+        if (i + NS + 1 < n) {
+          nx = tile_desc(P, pc);
+          if (++pc.k == pc.nt) cursor_next_group(P, pc);
+        }
+      }
+      cp_async_commit();
+      if (++slot == NS) slot = 0;
+      ++cc.k;
+      const bool ends = cc.k == cc.nt;
+      if (ends || i == n - 1) {
+        attn_sum<KV>(A);
+        const bool starts = seg_k == 0;
+        const long long gs = t0 + i + 1 - cc.k;
+        if (starts && ends) {
+          attn_write<KV>(P, A, cc.b, kvh);
+        } else {
+          PagedEntry e;
+          e.gid = cc.b * L.Hkv + cc.gi; e.gs = gs; e.ge = gs + cc.nt; e.pad = 0;
+          if (!starts) {
+            have_head = true;
+            he = e;
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+#pragma unroll
+              for (int w = 0; w < 4; ++w) sv[u][w] = A.acc[u][w];
+#pragma unroll
+            for (int w = 0; w < 2; ++w) { sv_m[w] = A.m[w]; sv_l[w] = A.l[w]; sv_mo[w] = A.mo[w]; }
+          } else {                                     // only at the end of the range
+            cp_async_wait<0>();
+            __syncwarp();
+            attn_store<KV>(A, reinterpret_cast<float*>(ring) + part_smem_floats(G), G);
+            if (lane == 0) ent[2 * warp + 1] = e;
+          }
+        }
+        seg_k = 0;
+        if (ends && i < n - 1) cursor_next_group(P, cc);
+      }
+    }
+    cp_async_wait<0>();
+    __syncwarp();
+    if (have_head) {
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) A.acc[u][w] = sv[u][w];
+#pragma unroll
+      for (int w = 0; w < 2; ++w) { A.m[w] = sv_m[w]; A.l[w] = sv_l[w]; A.mo[w] = sv_mo[w]; }
+      attn_store<KV>(A, reinterpret_cast<float*>(ring), G);
+      if (lane == 0) ent[2 * warp] = he;
+    }
+  }
+  __syncthreads();
+
+  // ---- the open ends of this CTA's warps, group by group in the order of the line
+  int* open_ent = reinterpret_cast<int*>(sm + S::kMisc);   // entry of the groups left open (2)
+  int n_open = 0;
+  for (int i = 0; i < 2 * NW;) {
+    const int gid = ent[i].gid;
+    if (gid < 0) { ++i; continue; }
+    int last = i;
+    for (int j = i + 1; j < 2 * NW; ++j) {
+      if (ent[j].gid == gid) last = j;
+      else if (ent[j].gid >= 0) break;
+    }
+    const long long gs = ent[i].gs, ge = ent[i].ge;
+    const bool whole = gs >= ct0 && ge <= ct1;
+    const int b = gid / L.Hkv, g = kv_head(L, gid % L.Hkv);
+    const int64_t head0 = (int64_t)b * L.Hq + (int64_t)g * G;
+    const int open_slot = gs < ct0 ? 0 : 1;
+    float* gp = P.part + (blockIdx.x * 2 + open_slot) * (int64_t)part_gmem_floats(G);
+    for (int o = tid; o < G * kD; o += NT) {
+      const int h = o >> 7, c = o & 127;
+      float M = -INFINITY, MO = -INFINITY;
+      for (int j = i; j <= last; ++j)
+        if (ent[j].gid == gid) {
+          const float* part = reinterpret_cast<const float*>(sm + (j >> 1) * NS * Cfg::kStageB) +
+                              (j & 1) * part_smem_floats(G);
+          M = fmaxf(M, part[G * kPartPitch + 3 * h]);
+          MO = fmaxf(MO, part[G * kPartPitch + 3 * h + 2]);
+        }
+      float Ls = 0.f, Ac = 0.f;
+      for (int j = i; j <= last; ++j)
+        if (ent[j].gid == gid) {
+          const float* part = reinterpret_cast<const float*>(sm + (j >> 1) * NS * Cfg::kStageB) +
+                              (j & 1) * part_smem_floats(G);
+          const float* ml = part + G * kPartPitch + 3 * h;
+          Ls += ml[1] * ex2_from(ml[0], M);
+          Ac += part[h * kPartPitch + c] * ex2_from(ml[2], MO);
+        }
+      if (whole) {
+        const float f = Ls > 0.f || Ls != Ls ? ex2_from(MO, M) / Ls : 0.f;
+        P.out[head0 * kD + o] = f2bf_rn(Ac * f);
+        if (P.lse && c == 0) P.lse[head0 + h] = (M + log2f(Ls)) * 0.6931471805599453f;
+      } else {
+        gp[o] = Ac;
+        if (c == 0) { gp[G * kD + 3 * h] = M; gp[G * kD + 3 * h + 1] = Ls; gp[G * kD + 3 * h + 2] = MO; }
+      }
+    }
+    if (!whole) { if (tid == 0) open_ent[n_open] = i; ++n_open; }
+    i = last + 1;
+  }
+  if (n_open == 0) return;
+  __threadfence();
+  __syncthreads();
+  // arrivals: a group that spans CTAs c0..c1 counts at c0's word, which wraps to zero
+  if (tid < n_open) {
+    const PagedEntry e = ent[open_ent[tid]];
+    const int c0 = (int)(((e.gs + 1) * PC - 1) / T), c1 = (int)((e.ge * PC - 1) / T);
+    const uint32_t old = atomicInc(P.arrive + c0, (uint32_t)(c1 - c0));
+    __threadfence();
+    open_ent[2 + tid] = old == (uint32_t)(c1 - c0) ? 1 : 0;
+  }
+  __syncthreads();
+  float* wt = reinterpret_cast<float*>(sm + S::kWt);          // [parts][8]
+  float* fac = reinterpret_cast<float*>(sm + S::kMisc) + 16;  // [8]
+  for (int x = 0; x < n_open; ++x) {
+    if (!open_ent[2 + x]) continue;
+    const PagedEntry e = ent[open_ent[x]];
+    const int c0 = (int)(((e.gs + 1) * PC - 1) / T), c1 = (int)((e.ge * PC - 1) / T);
+    const int np = c1 - c0 + 1;
+    const int64_t pf = part_gmem_floats(G);
+    // part i: the open end of CTA c0 + i (its last group for i = 0, its first otherwise)
+    const float* base = P.part + (int64_t)c0 * 2 * pf;
+    const int b = e.gid / L.Hkv, g = kv_head(L, e.gid % L.Hkv);
+    const int64_t head0 = (int64_t)b * L.Hq + (int64_t)g * G;
+    if (warp < G) {
+      float M = -INFINITY, MO = -INFINITY;
+      for (int i = lane; i < np; i += 32) {
+        const float* ml = base + (i * 2 + (i == 0)) * pf + G * kD + 3 * warp;
+        M = fmaxf(M, __ldcg(ml));
+        MO = fmaxf(MO, __ldcg(ml + 2));
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        MO = fmaxf(MO, __shfl_xor_sync(0xffffffffu, MO, o));
+      }
+      float Ls = 0.f;
+      for (int i = lane; i < np; i += 32) {
+        const float* ml = base + (i * 2 + (i == 0)) * pf + G * kD + 3 * warp;
+        Ls += __ldcg(ml + 1) * ex2_from(__ldcg(ml), M);
+        wt[i * 8 + warp] = ex2_from(__ldcg(ml + 2), MO);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) Ls += __shfl_xor_sync(0xffffffffu, Ls, o);
+      if (lane == 0) {
+        fac[warp] = Ls > 0.f || Ls != Ls ? ex2_from(MO, M) / Ls : 0.f;
+        if (P.lse) P.lse[head0 + warp] = (M + log2f(Ls)) * 0.6931471805599453f;
+      }
+    }
+    __syncthreads();
+    // four channels a thread; where G is small, thread teams share out the parts
+    const int items = G * (kD / 4), teams = NT / items;        // 1, 2, 4 or 8 teams
+    const int team = tid / items, it = tid % items, h = it >> 5;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = team; i < np; i += teams) {
+      const float4 a = __ldcg(reinterpret_cast<const float4*>(base + (i * 2 + (i == 0)) * pf) + it);
+      const float w = wt[i * 8 + h];
+      s.x = fmaf(a.x, w, s.x); s.y = fmaf(a.y, w, s.y);
+      s.z = fmaf(a.z, w, s.z); s.w = fmaf(a.w, w, s.w);
+    }
+    float4* red = reinterpret_cast<float4*>(sm);
+    red[tid] = s;
+    __syncthreads();
+    if (tid < items) {
+      for (int q = 1; q < teams; ++q) {
+        const float4 a = red[q * items + it];
+        s.x += a.x; s.y += a.y; s.z += a.z; s.w += a.w;
+      }
+      const float f = fac[h];
+      uint2 w;
+      w.x = pack_bf2(s.x * f, s.y * f);
+      w.y = pack_bf2(s.z * f, s.w * f);
+      *reinterpret_cast<uint2*>(P.out + head0 * kD + 4 * it) = w;
+    }
+    __syncthreads();
+  }
+}
+
+// ------------------------------------------------------------------ append of new tokens
+
+struct PagedAppendParams {
+  PagedPtrs C;
+  const uint16_t *k_pre, *v;
+  const int32_t *start_pos, *slot_map;
+  int64_t n_tok, cap_rows;       // B * n_new; n_pages * page
+  int n_new, Hkv;
+  int* status;
+  double theta[kD / 2];
+};
+
+// A CTA takes kPagedAppendTok consecutive tokens of the flattened [B][n_new] axis: their 64
+// angles once for all KV heads (sin and cos in double), then half a warp per (token, KV head)
+// row: 4 channel pairs a lane. Bound by HBM: 512 B read, 512 (264) B written per row.
+constexpr int kPagedAppendTok = 4;
+
+template <int KV>
+__global__ void __launch_bounds__(256)
+paged_append_kernel(const __grid_constant__ PagedAppendParams P) {
+  __shared__ double2 ang[kPagedAppendTok][kD / 2];
+  __shared__ int32_t slots[kPagedAppendTok];
+  const int tid = threadIdx.x;
+  const int64_t tok0 = (int64_t)blockIdx.x * kPagedAppendTok;
+  {
+    const int u = tid >> 6, i = tid & 63;
+    const int64_t tok = tok0 + u;
+    int slot = -1;
+    if (tok < P.n_tok) slot = P.slot_map[tok];
+    if (slot >= 0) {
+      const int64_t b = tok / P.n_new;
+      const int64_t pos = (int64_t)P.start_pos[b] + (tok - b * P.n_new);
+      if (slot >= P.cap_rows || pos < 0) {
+        if (i == 0) set_status(P.status, -6);
+        slot = -1;
+      } else {
+        double s, c;
+        rope_sincos((double)pos, P.theta[i], &s, &c);
+        ang[u][i] = make_double2(c, s);
+      }
+    }
+    if (i == 0) slots[u] = slot;
+  }
+  __syncthreads();
+  const int half = tid >> 4, ln = tid & 15;
+  for (int it = half; it < kPagedAppendTok * P.Hkv; it += 16) {
+    const int u = it / P.Hkv, g = it - u * P.Hkv;
+    const int slot = slots[u];
+    if (slot < 0) continue;
+    const int64_t src = ((tok0 + u) * P.Hkv + g) * kD;
+    const uint2 a = __ldg(reinterpret_cast<const uint2*>(P.k_pre + src) + ln);
+    const uint2 c = __ldg(reinterpret_cast<const uint2*>(P.k_pre + src + 64) + ln);
+    const uint4 vv = __ldg(reinterpret_cast<const uint4*>(P.v + src) + ln);
+    const float xa[4] = {bf_lo(a.x), bf_hi(a.x), bf_lo(a.y), bf_hi(a.y)};
+    const float xc[4] = {bf_lo(c.x), bf_hi(c.x), bf_lo(c.y), bf_hi(c.y)};
+    double lo[4], hi[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const double2 cs = ang[u][4 * ln + e];
+      lo[e] = (double)xa[e] * cs.x - (double)xc[e] * cs.y;
+      hi[e] = (double)xa[e] * cs.y + (double)xc[e] * cs.x;
+    }
+    const int64_t pid = slot >> P.C.lg;
+    const int64_t in = ((int64_t)g << P.C.lg) + (slot & ((1 << P.C.lg) - 1));
+    const int64_t row = pid * P.C.page_stride + in;
+    if (KV == kKvBf16) {
+      unsigned char* kd = P.C.k + row * 256;
+      uint2 w;
+      w.x = d2bf_rn(lo[0]) | (uint32_t)d2bf_rn(lo[1]) << 16;
+      w.y = d2bf_rn(lo[2]) | (uint32_t)d2bf_rn(lo[3]) << 16;
+      reinterpret_cast<uint2*>(kd)[ln] = w;
+      w.x = d2bf_rn(hi[0]) | (uint32_t)d2bf_rn(hi[1]) << 16;
+      w.y = d2bf_rn(hi[2]) | (uint32_t)d2bf_rn(hi[3]) << 16;
+      reinterpret_cast<uint2*>(kd + 128)[ln] = w;
+      reinterpret_cast<uint4*>(P.C.v + row * 256)[ln] = vv;
+    } else {
+      float k[8], y[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) { k[e] = (float)lo[e]; k[4 + e] = (float)hi[e]; }
+      unpack8(vv, y);
+      float mk = 0.f, mv = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) { mk = fmaxf(mk, fabsf(k[e])); mv = fmaxf(mv, fabsf(y[e])); }
+      const uint32_t team = 0xffffu << (tid & 16);
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1) {
+        mk = fmaxf(mk, __shfl_xor_sync(team, mk, o));
+        mv = fmaxf(mv, __shfl_xor_sync(team, mv, o));
+      }
+      const float sk = row_scale(mk), sv = row_scale(mv);
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float* z = e < 2 ? k : y;
+        const float s = e < 2 ? sk : sv;
+        const int j = 4 * (e & 1);
+        w[e] = f_e4m3x2(__fdiv_rn(z[j], s), __fdiv_rn(z[j + 1], s)) |
+               f_e4m3x2(__fdiv_rn(z[j + 2], s), __fdiv_rn(z[j + 3], s)) << 16;
+      }
+      unsigned char* kd = P.C.k + row * 128;
+      reinterpret_cast<uint32_t*>(kd)[ln] = w[0];
+      reinterpret_cast<uint32_t*>(kd + 64)[ln] = w[1];
+      reinterpret_cast<uint2*>(P.C.v + row * 128)[ln] = make_uint2(w[2], w[3]);
+      if (ln == 0) {
+        const int64_t srow = pid * ((int64_t)P.Hkv << P.C.lg) + in;
+        P.C.ks[srow] = sk;
+        P.C.vs[srow] = sv;
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ page reservation
+
+struct PagedReserveParams {
+  int32_t *free_pages, *table, *slot_map, *lens_out;
+  const int32_t *lens, *new_lens;
+  const int64_t* counters;
+  int64_t* counters_out;
+  int64_t cap;                   // tokens a table row can hold
+  int B, n_new, n_pages, stride, lg, chunks;
+  int* status;
+  uint32_t* arrive;
+};
+
+constexpr int kResThreads = 512;
+constexpr int kResTok = 2048, kResPages = 128;     // tokens and page moves of one warp item
+
+// saturating sum of counts (each at most 2^31 - 1)
+__device__ __forceinline__ uint32_t add_sat(uint32_t a, uint32_t b) { return min(a + b, 0x7fffffffu); }
+
+// Exclusive block-wide saturating sums of two counts; totals to tot[2]. scratch: 64 words.
+__device__ __forceinline__ void block_scan2(uint32_t& a, uint32_t& c, uint32_t* scratch,
+                                            uint32_t (&tot)[2]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t ia = a, ic = c;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t ua = __shfl_up_sync(0xffffffffu, ia, o), uc = __shfl_up_sync(0xffffffffu, ic, o);
+    if (lane >= o) { ia = add_sat(ia, ua); ic = add_sat(ic, uc); }
+  }
+  __syncthreads();
+  if (lane == 31) { scratch[warp] = ia; scratch[32 + warp] = ic; }
+  __syncthreads();
+  uint32_t ba = 0, bc = 0;
+  tot[0] = tot[1] = 0;
+  for (int w = 0; w < kResThreads / 32; ++w) {
+    if (w == warp) { ba = tot[0]; bc = tot[1]; }
+    tot[0] = add_sat(tot[0], scratch[w]);
+    tot[1] = add_sat(tot[1], scratch[32 + w]);
+  }
+  // exclusive: the neighbour's inclusive sum (a saturated one cannot be taken apart)
+  const uint32_t ea = __shfl_up_sync(0xffffffffu, ia, 1), ec = __shfl_up_sync(0xffffffffu, ic, 1);
+  a = add_sat(ba, lane ? ea : 0);
+  c = add_sat(bc, lane ? ec : 0);
+}
+
+// Every CTA computes the sums over the whole batch (B lengths from L2), then the warps of the
+// grid share out the (sequence, chunk) items: page moves between ring and table, and slots.
+// Nothing that a call reads is written before all CTAs have read it: the ring's taken and
+// returned entries are disjoint, held table entries are not rewritten, and the lengths and
+// counters are written by the CTA that arrives last, so they may be updated in place.
+__global__ void __launch_bounds__(kResThreads)
+paged_reserve_kernel(const __grid_constant__ PagedReserveParams P) {
+  extern __shared__ uint32_t rsm[];
+  uint32_t* upto = rsm;                      // [B] pages taken before each sequence
+  uint32_t* back = rsm + P.B;                // [B] pages returned before each sequence
+  __shared__ uint32_t scratch[64];
+  __shared__ uint32_t s_taken, s_bad, s_last;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int64_t head = P.counters[0], tail = P.counters[1];
+  const bool sane = head >= 0 && tail >= head && tail - head <= P.n_pages;
+  const uint32_t avail = sane ? (uint32_t)(tail - head) : 0;
+  const int ps1 = (1 << P.lg) - 1;
+  if (tid == 0) { s_taken = 0; s_bad = 0; }
+  __syncthreads();
+  uint32_t run_a = 0, run_c = 0;
+  for (int b0 = 0; b0 < P.B; b0 += kResThreads) {
+    const int b = b0 + tid;
+    uint32_t need = 0, ret = 0;
+    if (b < P.B) {
+      const int n0 = P.lens[b], n1 = P.new_lens[b];
+      if (n0 < 0 || n1 < 0 || n0 > P.cap || n1 > P.cap) {
+        s_bad = 1;
+      } else {
+        const int h0 = (int)(((int64_t)n0 + ps1) >> P.lg), h1 = (int)(((int64_t)n1 + ps1) >> P.lg);
+        if (h1 > h0) need = h1 - h0; else ret = h0 - h1;
+      }
+    }
+    uint32_t a = need, c = ret, tot[2];
+    block_scan2(a, c, scratch, tot);
+    a = add_sat(run_a, a);
+    c = add_sat(run_c, c);
+    if (b < P.B) {
+      upto[b] = a;
+      back[b] = c;
+      const uint32_t end = add_sat(a, need);
+      if (need && end <= avail) atomicMax(&s_taken, end);
+    }
+    run_a = add_sat(run_a, tot[0]);
+    run_c = add_sat(run_c, tot[1]);
+  }
+  __syncthreads();
+  // more pages than the ring has room for: the lengths or counters are not this pool's
+  const bool ok = sane && (int64_t)avail + run_c <= P.n_pages;
+  if (tid == 0 && blockIdx.x == 0 && (!ok || s_bad)) set_status(P.status, -6);
+  const int hm = ok ? (int)(head % P.n_pages) : 0, tm = ok ? (int)(tail % P.n_pages) : 0;
+  const int warps = gridDim.x * (kResThreads / 32);
+  const int64_t items = (int64_t)P.B * P.chunks;
+  for (int64_t it = (int64_t)blockIdx.x * (kResThreads / 32) + (tid >> 5); it < items; it += warps) {
+    const int b = (int)(it / P.chunks), ch = (int)(it - (int64_t)b * P.chunks);
+    int n0 = P.lens[b], n1 = P.new_lens[b];
+    if (n0 < 0 || n1 < 0 || n0 > P.cap || n1 > P.cap) n1 = n0 = 0;     // no slots, no moves
+    const int h0 = (int)(((int64_t)n0 + ps1) >> P.lg), h1 = (int)(((int64_t)n1 + ps1) >> P.lg);
+    const int64_t u0 = upto[b], r0 = back[b];
+    const bool granted = ok && (h1 <= h0 || u0 + (h1 - h0) <= avail);
+    if (!granted) n1 = n0;
+    int32_t* row = P.table + (int64_t)b * P.stride;
+    if (granted) {
+      const int m1 = min(abs(h1 - h0), (ch + 1) * kResPages);
+      for (int j = ch * kResPages + lane; j < m1; j += 32) {
+        if (h1 > h0) {
+          int64_t at = hm + u0 + j;
+          if (at >= P.n_pages) at -= P.n_pages;
+          row[h0 + j] = P.free_pages[at];
+        } else {
+          int64_t at = tm + r0 + j;
+          if (at >= P.n_pages) at -= P.n_pages;
+          P.free_pages[at] = row[h1 + j];
+        }
+      }
+    }
+    const int t1 = min(P.n_new, (ch + 1) * kResTok);
+    int32_t* slots = P.slot_map + (int64_t)b * P.n_new;
+    for (int j = ch * kResTok + lane; j < t1; j += 32) {
+      const int64_t pos = (int64_t)n0 + j;
+      int slot = -1;
+      if (pos < n1) {
+        const int pg = (int)(pos >> P.lg);
+        int id;
+        if (pg < h0) {
+          id = row[pg];
+        } else {
+          int64_t at = hm + u0 + (pg - h0);
+          if (at >= P.n_pages) at -= P.n_pages;
+          id = P.free_pages[at];
+        }
+        slot = (id << P.lg) + (int)(pos & ps1);
+      }
+      slots[j] = slot;
+    }
+  }
+  // lengths and counters, once every CTA has read them
+  __syncthreads();
+  if (tid == 0) s_last = gridDim.x == 1 || atomicInc(P.arrive, gridDim.x - 1) == gridDim.x - 1;
+  __syncthreads();
+  if (!s_last) return;
+  for (int b = tid; b < P.B; b += kResThreads) {
+    const int n0 = P.lens[b], n1 = P.new_lens[b];
+    int n = n0;
+    if (ok && !(n0 < 0 || n1 < 0 || n0 > P.cap || n1 > P.cap)) {
+      const int h0 = (int)(((int64_t)n0 + ps1) >> P.lg), h1 = (int)(((int64_t)n1 + ps1) >> P.lg);
+      if (h1 <= h0 || (int64_t)upto[b] + (h1 - h0) <= avail) n = n1;
+    }
+    P.lens_out[b] = n;
+  }
+  if (tid == 0) {
+    P.counters_out[0] = ok ? head + s_taken : head;
+    P.counters_out[1] = ok ? tail + run_c : tail;
+  }
+}
+
+}  // namespace rtp

@@ -1,5 +1,6 @@
-"""One decode layer's device memory (caches, workspace) allocated with PyTorch, driving
-librtp through the C ABI. Allocation and stream plumbing only; no arithmetic of the method."""
+"""A decode layer's device memory (caches, workspace) allocated with PyTorch, driving librtp
+through the C ABI: DecodeLayer over contiguous caches, PageTable and PagedLayer over paged ones.
+Allocation and stream plumbing only; no arithmetic of the method."""
 from __future__ import annotations
 
 import numpy as np
@@ -83,6 +84,108 @@ class DecodeLayer:
             buf = torch.empty(need + 256, dtype=torch.uint8, device=q_pre.device)
             off = (-buf.data_ptr()) % 256
             self.pf_ws = buf[off:off + need]
+        return rtp.rtp_prefill(self.desc, q_pre, k_pre, v, n_b, n_max, out, self.pf_ws,
+                               self.pf_ws.numel(), stream)
+
+    def status(self, stream=None) -> int:
+        return rtp.rtp_read_device_status(self.ws, stream)
+
+
+def _workspace(n, device):
+    """n bytes at a 256-byte boundary."""
+    buf = torch.empty(n + 256, dtype=torch.uint8, device=device)
+    off = (-buf.data_ptr()) % 256
+    return buf[off:off + n]
+
+
+class PageTable:
+    """The pages of a batch of B sequences, shared by the layers of a model: lengths, block
+    table and ring of free pages, all on the GPU. A sequence holds at most max_seq_len tokens."""
+
+    def __init__(self, B, n_pages, page_size, max_seq_len, device="cuda"):
+        i32 = dict(dtype=torch.int32, device=device)
+        self.B, self.n_pages, self.page_size = B, n_pages, page_size
+        self.lens = torch.zeros(B, **i32)
+        self.block_table = torch.zeros((B, max(1, -(-max_seq_len // page_size))), **i32)
+        self.free_pages = torch.arange(n_pages, **i32)
+        self.counters = torch.tensor([0, n_pages], dtype=torch.int64, device=device)
+        self.pool = rtp.make_page_pool(self.free_pages, self.block_table, page_size)
+        self.ws = _workspace(rtp.RTP_PAGED_CTRL_BYTES, device)
+        rtp.rtp_paged_workspace_init(self.ws)
+
+    def reserve(self, new_lens, slot_map=None, stream=None):
+        """Takes or returns pages so that sequence b holds new_lens[b] tokens (int32 [B]; 0 ends
+        it) and writes the slots of its new tokens to slot_map (int32 [B][n_new]). Updates lens
+        in place: a sequence that the free pages do not suffice for keeps its length."""
+        n_new = 0 if slot_map is None else slot_map.shape[1]
+        return rtp.rtp_paged_reserve(self.pool, self.lens, new_lens, self.counters, self.lens,
+                                     self.counters, slot_map, n_new, self.ws, stream)
+
+    def status(self, stream=None) -> int:
+        return rtp.rtp_read_device_status(self.ws, stream)
+
+
+class PagedLayer:
+    """One layer's K/V pages over a PageTable. kv_dtype: torch.bfloat16, or torch.float8_e4m3fn
+    with a scale per row."""
+
+    def __init__(self, table: PageTable, Hq, Hkv, sinks, window, max_seq_len, ret_mask,
+                 kv_dtype=torch.bfloat16, rope_base=1e6):
+        device = table.block_table.device
+        self.table, self.B, self.Hq, self.Hkv = table, table.B, Hq, Hkv
+        slots, self.n_ret, self.n_loc = rtp.rtp_build_slot_map(ret_mask)
+        self.desc = rtp.LayerDesc(table.B, Hq, Hkv, sinks, window, max_seq_len, slots, rope_base)
+        shape = (table.n_pages, Hkv, table.page_size, 128)
+        self.k = torch.empty(shape, dtype=kv_dtype, device=device)
+        self.v = torch.empty(shape, dtype=kv_dtype, device=device)
+        self.k_scale = self.v_scale = None
+        if kv_dtype is not torch.bfloat16:
+            self.k_scale = torch.empty(shape[:3], dtype=torch.float32, device=device)
+            self.v_scale = torch.empty(shape[:3], dtype=torch.float32, device=device)
+        self.cache = rtp.make_paged_cache(self.k, self.v, table.block_table, self.k_scale,
+                                          self.v_scale)
+        n = rtp.rtp_paged_workspace_bytes(self.desc)
+        if n == 0:
+            raise ValueError("librtp rejected the layer description")
+        self.ws = _workspace(n, device)
+        rtp.rtp_paged_workspace_init(self.ws)
+        self.zeros = torch.zeros(table.B, dtype=torch.int32, device=device)
+        self.pf_ws = None
+
+    def append(self, k_pre, v, start_pos, slot_map, stream=None):
+        """k_pre, v: bf16 [B][n_new][Hkv][128]; start_pos: int32 [B], the lengths before the
+        reservation that filled slot_map (int32 [B][n_new])."""
+        return rtp.rtp_paged_append_kv(self.desc, self.cache, k_pre, v, start_pos, slot_map,
+                                       k_pre.shape[1], self.ws, stream)
+
+    def decode(self, q_pre, seq_lens, out, lse=None, stream=None):
+        return rtp.rtp_paged_decode_step(self.desc, self.cache, q_pre, seq_lens, out, lse, self.ws,
+                                         stream)
+
+    def decode_append(self, k_new, v_new, q_pre, seq_lens, out, lse=None, stream=None):
+        """Append of the decode token (k_new, v_new: bf16 [B][Hkv][128] at seq_lens - 1, whose
+        page is reserved) and the decode step in one launch."""
+        return rtp.rtp_paged_decode_step_append(self.desc, self.cache, k_new, v_new, q_pre,
+                                                seq_lens, out, lse, self.ws, stream)
+
+    def prefill(self, q_pre, k_pre, v, n_b, slot_map, out, stream=None):
+        """Prompts of n_b[b] tokens at positions 0..n_b[b]-1 of sequences that were just reserved
+        with slot_map (int32 [B][n_max]): appends their K/V to the pages, then writes the causal
+        prefill attention to out, as DecodeLayer.prefill. The prefill attends to the bf16 keys
+        and values of the prompt, whatever the cache holds."""
+        n_max = q_pre.shape[1]
+        rtp.rtp_paged_append_kv(self.desc, self.cache, k_pre, v, self.zeros, slot_map, n_max,
+                                self.ws, stream)
+        need = rtp.rtp_prefill_workspace_bytes(self.desc, n_max)
+        if need == 0:
+            raise ValueError("librtp rejected the prompt length")
+        if self.pf_ws is None or self.pf_ws.numel() < need:
+            self.pf_ws = _workspace(need, q_pre.device)
+        # a later, longer prompt lets go of this buffer: not before this call's stream is done
+        used = torch.cuda.current_stream() if stream is None else stream
+        if not hasattr(used, "cuda_stream"):
+            used = torch.cuda.ExternalStream(int(used))
+        self.pf_ws.record_stream(used)
         return rtp.rtp_prefill(self.desc, q_pre, k_pre, v, n_b, n_max, out, self.pf_ws,
                                self.pf_ws.numel(), stream)
 

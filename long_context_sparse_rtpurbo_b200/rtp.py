@@ -12,7 +12,8 @@ import numpy as np
 import torch
 
 from . import _lib
-from ._lib import RtpCache, RtpLayerDesc, RTP_OK
+from ._lib import (RTP_KV_BF16, RTP_KV_E4M3, RTP_OK, RTP_PAGED_CTRL_BYTES, RtpCache,  # noqa: F401
+                   RtpLayerDesc, RtpPagedCache, RtpPagePool)
 
 
 class RtpError(RuntimeError):
@@ -141,6 +142,177 @@ def rtp_prefill(desc: LayerDesc, q_pre, k_pre, v, n_b, n_max, out, ws=None, ws_b
     return _check("rtp_prefill", _lib.load().rtp_prefill(
         desc.ref, _ptr(q_pre), _ptr(k_pre), _ptr(v), _ptr(n_b), int(n_max), _ptr(out), _ptr(ws),
         int(ws_bytes), _stream(stream)))
+
+
+# ------------------------------------------------------------------------------- paged caches
+# The calls below check dtype, size, contiguity and device of every tensor: a paged call is cheap
+# enough to be made with the wrong one of many buffers. All tensors must be on the current device.
+
+def _arg(t: torch.Tensor, what: str, dtype, n: int, dev: int, optional=False) -> int | None:
+    if t is None and optional:
+        return None
+    if t.dtype is not dtype or t.numel() != n or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{what}: a contiguous {dtype} tensor of {n} elements on cuda:{dev} is "
+                         f"wanted, got {tuple(t.shape)} {t.dtype} on {t.device}")
+    return t.data_ptr()
+
+
+def _ws_arg(ws: torch.Tensor, dev: int) -> tuple[int | None, int]:
+    if ws is None:
+        return None, 0
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"workspace: a contiguous tensor on cuda:{dev} is wanted")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _stream_on(stream, dev: int) -> int:
+    if torch.cuda.current_device() != dev:
+        raise ValueError(f"tensors are on cuda:{dev}, which is not the current device")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+class PagedCache:
+    """A paged cache of one layer (see make_paged_cache): owns the tensors that its struct points
+    to."""
+
+    def __init__(self, k, v, block_table, k_scale=None, v_scale=None):
+        if k.dim() != 4 or k.shape[3] != 128 or k.shape != v.shape or k.stride() != v.stride():
+            raise ValueError("k and v: [n_pages][Hkv][page_size][128] tensors of equal strides")
+        n_pages, Hkv, page, _ = k.shape
+        block = Hkv * page
+        if k.stride()[1:] != (page * 128, 128, 1) or (n_pages > 1 and k.stride(0) % 128):
+            raise ValueError("the rows of a page must be dense and pages a whole number of rows apart")
+        e4m3 = k.dtype in (torch.uint8, torch.float8_e4m3fn)
+        if v.dtype is not k.dtype or not (e4m3 or k.dtype is torch.bfloat16):
+            raise ValueError("k and v are both bfloat16, or both e4m3 (float8_e4m3fn or uint8)")
+        dev = k.get_device()
+        if e4m3 != (k_scale is not None) or e4m3 != (v_scale is not None):
+            raise ValueError("k_scale and v_scale go with an e4m3 cache, and only with one")
+        if v.get_device() != dev:
+            raise ValueError("k and v are on different devices")
+        n = n_pages * block
+        if block_table.dim() != 2:
+            raise ValueError("block_table: [B][entries]")
+        self.B, self.table_stride = block_table.shape
+        self.Hkv, self.page_size, self.n_pages, self.device_index = Hkv, page, n_pages, dev
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.block_table = block_table
+        self.c = RtpPagedCache(
+            RTP_KV_E4M3 if e4m3 else RTP_KV_BF16, page, n_pages, self.table_stride, k.data_ptr(),
+            v.data_ptr(), _arg(k_scale, "k_scale", torch.float32, n, dev, True),
+            _arg(v_scale, "v_scale", torch.float32, n, dev, True),
+            k.stride(0) // 128 if n_pages > 1 else 0,
+            _arg(block_table, "block_table", torch.int32, self.B * self.table_stride, dev))
+        self.ref = ctypes.byref(self.c)
+
+
+def make_paged_cache(k, v, block_table, k_scale=None, v_scale=None) -> PagedCache:
+    """The paged cache of one layer. k, v: [n_pages][Hkv][page_size][128] in bf16, or e4m3 with
+    k_scale and v_scale (float [n_pages][Hkv][page_size]); the page axis may have a stride (K and
+    V interleaved in one allocation). block_table: int32 [B][entries]."""
+    return PagedCache(k, v, block_table, k_scale, v_scale)
+
+
+class PagePoolRef:
+    """The rtp_page_pool of a batch: owns the tensors that it points to."""
+
+    def __init__(self, free_pages, block_table, page_size):
+        if block_table.dim() != 2:
+            raise ValueError("block_table: [B][entries]")
+        self.B, self.table_stride = block_table.shape
+        self.n_pages, self.device_index = free_pages.numel(), free_pages.get_device()
+        self.free_pages, self.block_table = free_pages, block_table
+        dev = self.device_index
+        self.c = RtpPagePool(
+            self.B, int(page_size), self.n_pages, self.table_stride,
+            _arg(free_pages, "free_pages", torch.int32, self.n_pages, dev),
+            _arg(block_table, "block_table", torch.int32, self.B * self.table_stride, dev))
+        self.ref = ctypes.byref(self.c)
+
+
+def make_page_pool(free_pages, block_table, page_size) -> PagePoolRef:
+    """free_pages: int32 [n_pages], the ring of free page ids; block_table: int32 [B][entries]."""
+    return PagePoolRef(free_pages, block_table, page_size)
+
+
+def rtp_paged_workspace_bytes(desc: LayerDesc) -> int:
+    return int(_lib.load().rtp_paged_workspace_bytes(desc.ref))
+
+
+def rtp_paged_workspace_init(ws: torch.Tensor, stream=None):
+    """Once after allocating a workspace of the paged calls (256-byte aligned)."""
+    return _check("rtp_paged_workspace_init", _lib.load().rtp_paged_workspace_init(
+        _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def rtp_paged_reserve(pool: PagePoolRef, lens, new_lens, counters, lens_out, counters_out, slot_map,
+                      n_new, ws, stream=None):
+    """Block tables and slot maps for new lengths (see include/rtp.h). lens, new_lens, lens_out:
+    int32 [B]; counters, counters_out: int64 [2]; slot_map: int32 [B][n_new]."""
+    B, dev = pool.B, pool.device_index
+    w, wb = _ws_arg(ws, dev)
+    return _check("rtp_paged_reserve", _lib.load().rtp_paged_reserve(
+        pool.ref, _arg(lens, "lens", torch.int32, B, dev),
+        _arg(new_lens, "new_lens", torch.int32, B, dev),
+        _arg(counters, "counters", torch.int64, 2, dev),
+        _arg(lens_out, "lens_out", torch.int32, B, dev),
+        _arg(counters_out, "counters_out", torch.int64, 2, dev),
+        _arg(slot_map, "slot_map", torch.int32, B * n_new, dev, n_new == 0), n_new, w, wb,
+        _stream_on(stream, dev)))
+
+
+def rtp_paged_append_kv(desc: LayerDesc, cache: PagedCache, k_pre, v, start_pos, slot_map, n_new,
+                        ws=None, stream=None):
+    """New tokens to their slots (see include/rtp.h). k_pre, v: bf16 [B][n_new][Hkv][128];
+    start_pos: int32 [B]; slot_map: int32 [B][n_new]."""
+    B, dev = desc.c.B, cache.device_index
+    _paged_fits(desc, cache)
+    n = B * n_new * cache.Hkv * 128
+    return _check("rtp_paged_append_kv", _lib.load().rtp_paged_append_kv(
+        desc.ref, cache.ref, _arg(k_pre, "k_pre", torch.bfloat16, n, dev),
+        _arg(v, "v", torch.bfloat16, n, dev), _arg(start_pos, "start_pos", torch.int32, B, dev),
+        _arg(slot_map, "slot_map", torch.int32, B * n_new, dev), n_new, _ws_arg(ws, dev)[0],
+        _stream_on(stream, dev)))
+
+
+def _paged_fits(desc: LayerDesc, cache: PagedCache):
+    if cache.Hkv != desc.c.Hkv or cache.B != desc.c.B:
+        raise ValueError(f"a cache of {cache.Hkv} KV heads and {cache.B} sequences does not go with "
+                         f"a description of {desc.c.Hkv} and {desc.c.B}")
+
+
+def rtp_paged_decode_step(desc: LayerDesc, cache: PagedCache, q_pre, seq_lens, out, lse=None, ws=None,
+                          stream=None):
+    """Decode step of one layer over a paged cache (see include/rtp.h). q_pre, out: bf16
+    [B][Hq][128]; seq_lens: int32 [B]; lse: float [B][Hq] or None."""
+    c, dev = desc.c, cache.device_index
+    _paged_fits(desc, cache)
+    n = c.B * c.Hq
+    w, wb = _ws_arg(ws, dev)
+    return _check("rtp_paged_decode_step", _lib.load().rtp_paged_decode_step(
+        desc.ref, cache.ref, _arg(q_pre, "q_pre", torch.bfloat16, n * 128, dev),
+        _arg(seq_lens, "seq_lens", torch.int32, c.B, dev),
+        _arg(out, "out", torch.bfloat16, n * 128, dev),
+        _arg(lse, "lse", torch.float32, n, dev, True), w, wb, _stream_on(stream, dev)))
+
+
+def rtp_paged_decode_step_append(desc: LayerDesc, cache: PagedCache, k_new, v_new, q_pre, seq_lens,
+                                 out, lse=None, ws=None, stream=None):
+    """The decode token's append and the decode step in one launch (see include/rtp.h). k_new,
+    v_new: bf16 [B][Hkv][128]; the others as rtp_paged_decode_step."""
+    c, dev = desc.c, cache.device_index
+    _paged_fits(desc, cache)
+    n, m = c.B * c.Hq, c.B * c.Hkv * 128
+    w, wb = _ws_arg(ws, dev)
+    return _check("rtp_paged_decode_step_append", _lib.load().rtp_paged_decode_step_append(
+        desc.ref, cache.ref, _arg(k_new, "k_new", torch.bfloat16, m, dev),
+        _arg(v_new, "v_new", torch.bfloat16, m, dev),
+        _arg(q_pre, "q_pre", torch.bfloat16, n * 128, dev),
+        _arg(seq_lens, "seq_lens", torch.int32, c.B, dev),
+        _arg(out, "out", torch.bfloat16, n * 128, dev),
+        _arg(lse, "lse", torch.float32, n, dev, True), w, wb, _stream_on(stream, dev)))
 
 
 def rtp_decode_step_static(desc: LayerDesc, cache: RtpCache, q_pre, w_qidx, seq_lens, p, out,
