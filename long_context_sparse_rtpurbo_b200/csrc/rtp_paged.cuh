@@ -55,7 +55,7 @@ template <> struct PagedCfg<kKvBf16> {
   static constexpr int kStageB = 16 * 512;
 };
 template <> struct PagedCfg<kKvE4m3> {
-  static constexpr int kWarps = 8, kStages = 5, kRowB = 128, kTerms = 2;
+  static constexpr int kWarps = 12, kStages = 4, kRowB = 128, kTerms = 2;
   static constexpr int kStageB = 16 * 256 + 128;
 };
 
@@ -74,15 +74,22 @@ struct PagedEntry {              // an open end of a warp's range
 template <int KV>
 struct PagedSmem {
   using Cfg = PagedCfg<KV>;
+  static constexpr int kEntries = 2 * Cfg::kWarps;
   static constexpr int kRing = Cfg::kWarps * Cfg::kStages * Cfg::kStageB;
-  static constexpr int kAng = kRing;                               // [warps][64] (cos, sin)
+  static constexpr int kTheta = kRing;                             // [64] doubles
+  static constexpr int kAng = kTheta + 64 * 8;                     // [warps][64] (cos, sin)
   static constexpr int kMask = kAng + Cfg::kWarps * 64 * 8;        // [warps][8] row masks
   static constexpr int kEnt = kMask + Cfg::kWarps * 8 * 4;
-  static constexpr int kPrefix = kEnt + Cfg::kWarps * 2 * (int)sizeof(PagedEntry);
+  static constexpr int kRun = kEnt + kEntries * (int)sizeof(PagedEntry);   // [entries] PagedRun
+  static constexpr int kEw = kRun + kEntries * 16;                 // [entries][8] weights
+  static constexpr int kMl = kEw + kEntries * 8 * 4;               // [entries][8] (M, L, MO, factor)
+  static constexpr int kPrefix = kMl + kEntries * 8 * 16;
   static constexpr int kMisc = kPrefix + 130 * 8;
   static constexpr int kWt = kMisc + 256;                          // [160][8] weights of a merge
   static constexpr int kBytes = kWt + kPagedMaxCTAs * 8 * 4;
 };
+// entries of one group in a CTA: the first, all of them (bits), whether the group is complete
+struct PagedRun { int first; uint32_t members; int whole, slot; };
 
 // ------------------------------------------------------------------ conversions and products
 
@@ -204,27 +211,15 @@ __device__ __forceinline__ void cursor_next_group(const PagedDecodeParams& P, Cu
   }
   cursor_group(P.L, c);
 }
-// The cursor of tile t (< the number of tiles); prefix: tiles before each 32 sequences.
-__device__ __forceinline__ Cursor cursor_at(const PagedDecodeParams& P, const long long* prefix,
-                                            long long t) {
-  const int lane = threadIdx.x & 31, nc = (P.L.B + 31) >> 5;
-  int before = 0;                              // chunks that start at or before t
-  for (int i = lane; i < nc; i += 32) before += prefix[i] <= t;
-  before = __reduce_add_sync(0xffffffffu, before);
+// The cursor of the tile that is rel tiles after the start of a chunk of 32 sequences; lens: this
+// lane's length of the chunk, incl and mine: its tiles with and without the lanes before.
+__device__ __forceinline__ Cursor cursor_at(const PagedDecodeParams& P, int chunk, long long rel,
+                                            int lens, long long incl, long long mine) {
   Cursor c;
-  const int chunk = before - 1;
-  c.lens = paged_len(P, chunk * 32 + lane, nullptr);
-  const long long mine = seq_tiles(P.L, c.lens);
-  long long incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long u = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += u;
-  }
-  const long long rel = t - prefix[chunk];
+  c.lens = lens;
   const int j = __popc(__ballot_sync(0xffffffffu, incl <= rel));
   c.b = chunk * 32 + j;
-  c.n = __shfl_sync(0xffffffffu, c.lens, j);
+  c.n = __shfl_sync(0xffffffffu, lens, j);
   const int in_seq = (int)(rel - __shfl_sync(0xffffffffu, incl - mine, j));
   const int tr = (c.n + 15) >> 4;
   if (in_seq < P.L.n_ret * tr) {
@@ -237,6 +232,15 @@ __device__ __forceinline__ Cursor cursor_at(const PagedDecodeParams& P, const lo
   }
   cursor_group(P.L, c);
   return c;
+}
+__device__ __forceinline__ long long warp_incl_sum(long long x) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += u;
+  }
+  return x;
 }
 
 struct TileDesc { int pid, row; uint32_t mask; };   // page, row in the page block, rows attended
@@ -320,47 +324,62 @@ __device__ __forceinline__ void attn_reset(PagedAttn<KV>& A) {
   for (int e = 0; e < 2; ++e) { A.m[e] = -INFINITY; A.mo[e] = -INFINITY; A.l[e] = 0.f; }
 }
 
-// (cos, sin) of the query position's 64 angles into this warp's table
-__device__ __forceinline__ void fill_angles(const LayerShape& L, float2* ang, int pos) {
+// (cos, sin) of the query position's 64 angles into this warp's table. theta lies in shared
+// memory: lanes that read different words of the parameters would be served one by one.
+__device__ __forceinline__ void fill_angles(const double* theta, float2* ang, int pos) {
   const int lane = threadIdx.x & 31;
   __syncwarp();
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     float s, c;
-    rope_sincosf((double)pos, L.theta[lane + 32 * e], &s, &c);
+    rope_sincosf((double)pos, theta[lane + 32 * e], &s, &c);
     ang[lane + 32 * e] = make_float2(c, s);
   }
   __syncwarp();
+}
+
+// This lane's channels of the head's query: pairs c..c+1 (and 64 on) of the first and second
+// half of each 16-channel step of the products.
+template <int KV>
+__device__ __forceinline__ int query_channel(int kk, int e) {
+  const int t = threadIdx.x & 3;
+  return KV == kKvBf16 ? 16 * kk + 2 * t + 8 * e : 16 * kk + 4 * t + 2 * e;
+}
+struct QueryRaw { uint32_t lo[8], hi[8]; };
+template <int KV>
+__device__ __forceinline__ void query_fetch(const PagedDecodeParams& P, QueryRaw& R, int b, int g) {
+  const int h = (threadIdx.x & 31) >> 2, G = P.L.G;
+  const uint16_t* q = P.q_pre + ((int64_t)b * P.L.Hq + (int64_t)g * G + min(h, G - 1)) * kD;
+#pragma unroll
+  for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int i = query_channel<KV>(kk, e);
+      R.lo[2 * kk + e] = __ldg(reinterpret_cast<const uint32_t*>(q + i));
+      R.hi[2 * kk + e] = __ldg(reinterpret_cast<const uint32_t*>(q + i + 64));
+    }
 }
 
 // R(m) q log2(e) / sqrt(128) of the G heads as B fragments. bf16 cache: three bf16 terms (24
 // bits). e4m3 cache: two fp16 terms (22 bits) of the query divided by a power of two that
 // brings its largest element into [1, 2), since fp16 has few exponents.
 template <int KV>
-__device__ __forceinline__ void load_query(const PagedDecodeParams& P, PagedAttn<KV>& A, int b,
-                                           int g, const float2* ang) {
+__device__ __forceinline__ void query_terms(PagedAttn<KV>& A, const QueryRaw& R, const float2* ang,
+                                            int G) {
   const int lane = threadIdx.x & 31, h = lane >> 2, t = lane & 3;
-  const int G = P.L.G;
   const float sc = kLog2e * 0.08838834764831845f;      // 1 / sqrt(128)
-  const uint16_t* q = P.q_pre + ((int64_t)b * P.L.Hq + (int64_t)g * G + min(h, G - 1)) * kD;
   float x[8][4];
 #pragma unroll
-  for (int kk = 0; kk < 4; ++kk) {
-    // channels c..c+1 and c2..c2+1 of this lane in the step's first and second half
-    const int c = KV == kKvBf16 ? 16 * kk + 2 * t : 16 * kk + 4 * t;
-    const int c2 = KV == kKvBf16 ? c + 8 : c + 2;
+  for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int i = e ? c2 : c;
-      const uint32_t lo = *reinterpret_cast<const uint32_t*>(q + i);
-      const uint32_t hi = *reinterpret_cast<const uint32_t*>(q + i + 64);
-      const float4 a = *reinterpret_cast<const float4*>(ang + i);
+      const uint32_t lo = R.lo[2 * kk + e], hi = R.hi[2 * kk + e];
+      const float4 a = *reinterpret_cast<const float4*>(ang + query_channel<KV>(kk, e));
       x[kk][2 * e] = (bf_lo(lo) * a.x - bf_lo(hi) * a.y) * sc;
       x[kk][2 * e + 1] = (bf_hi(lo) * a.z - bf_hi(hi) * a.w) * sc;
       x[kk + 4][2 * e] = (bf_lo(lo) * a.y + bf_lo(hi) * a.x) * sc;
       x[kk + 4][2 * e + 1] = (bf_hi(lo) * a.w + bf_hi(hi) * a.z) * sc;
     }
-  }
   if (h >= G) {
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk)
@@ -626,8 +645,9 @@ __device__ __forceinline__ void attn_store(const PagedAttn<KV>& A, float* dst, i
 // Writes the decode token's key and value of KV head g at its page row and into its row of the
 // staged tile (one warp). The rotation and the roundings are those of the bulk append.
 template <int KV>
-__device__ __noinline__ void paged_append_row(const PagedDecodeParams& P, int b, int g, int pos,
-                                              int64_t row, int64_t srow, uint32_t stage) {
+__device__ __noinline__ void paged_append_row(const PagedDecodeParams& P, const double* theta, int b,
+                                              int g, int pos, int64_t row, int64_t srow,
+                                              uint32_t stage) {
   using Cfg = PagedCfg<KV>;
   const int lane = threadIdx.x & 31, r = pos & 15;
   const uint16_t* kp = P.k_new + ((int64_t)b * P.L.Hkv + g) * kD;
@@ -644,7 +664,7 @@ __device__ __noinline__ void paged_append_row(const PagedDecodeParams& P, int b,
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     double sn, cs;
-    rope_sincos((double)pos, P.L.theta[2 * lane + e], &sn, &cs);
+    rope_sincos((double)pos, theta[2 * lane + e], &sn, &cs);
     const double xa = e ? bf_hi(a) : bf_lo(a), xb = e ? bf_hi(c) : bf_lo(c);
     lo[e] = xa * cs - xb * sn;
     hi[e] = xa * sn + xb * cs;
@@ -693,6 +713,22 @@ __device__ __noinline__ void paged_append_row(const PagedDecodeParams& P, int b,
 
 // ------------------------------------------------------------------ the kernel
 
+// Outputs of the sequences of a chunk that have no tiles (each by one CTA), and the report of
+// lengths out of range. One warp.
+__device__ __noinline__ void paged_idle(const PagedDecodeParams& P, int ch, int len, bool bad) {
+  const int lane = threadIdx.x & 31, b = ch * 32 + lane;
+  if (bad && blockIdx.x == 0) set_status(P.status, -6);
+  uint32_t none = __ballot_sync(0xffffffffu, b < P.L.B && len == 0 && b % gridDim.x == blockIdx.x);
+  while (none) {
+    const int64_t e = ch * 32 + __ffs(none) - 1;
+    none &= none - 1;
+    uint4* o = reinterpret_cast<uint4*>(P.out + e * P.L.Hq * kD);
+    for (int i = lane; i < P.L.Hq * (kD / 8); i += 32) o[i] = make_uint4(0, 0, 0, 0);
+    if (P.lse)
+      for (int i = lane; i < P.L.Hq; i += 32) P.lse[e * P.L.Hq + i] = -INFINITY;
+  }
+}
+
 template <int KV, bool APPEND>
 __global__ void __launch_bounds__(PagedCfg<KV>::kWarps * 32, 1)
 paged_decode_kernel(const __grid_constant__ PagedDecodeParams P) {
@@ -705,62 +741,71 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams P) {
   const int G = L.G;
   long long* prefix = reinterpret_cast<long long*>(sm + S::kPrefix);
   PagedEntry* ent = reinterpret_cast<PagedEntry*>(sm + S::kEnt);
+  double* theta = reinterpret_cast<double*>(sm + S::kTheta);
   float2* ang = reinterpret_cast<float2*>(sm + S::kAng) + warp * 64;
   uint32_t* masks = reinterpret_cast<uint32_t*>(sm + S::kMask) + warp * 8;
 
-  // ---- tiles before each 32 sequences; outputs of sequences that have none
+  // ---- the line: tiles before each 32 sequences, and in all. Up to 32 sequences: every warp
+  // makes the sums itself.
   const int nc = (L.B + 31) >> 5;
-  for (int ch = warp; ch < nc; ch += NW) {
-    const int b = ch * 32 + lane;
-    bool bad = false;
-    const int n = paged_len(P, b, &bad);
-    if (bad && blockIdx.x == 0) set_status(P.status, -6);
-    long long t = seq_tiles(L, n);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-    if (lane == 0) prefix[ch] = t;
-    uint32_t none = __ballot_sync(0xffffffffu, b < L.B && n == 0 && b % gridDim.x == blockIdx.x);
-    while (none) {
-      const int64_t e = ch * 32 + __ffs(none) - 1;
-      none &= none - 1;
-      uint4* o = reinterpret_cast<uint4*>(P.out + e * L.Hq * kD);
-      for (int i = lane; i < L.Hq * (kD / 8); i += 32) o[i] = make_uint4(0, 0, 0, 0);
-      if (P.lse)
-        for (int i = lane; i < L.Hq; i += 32) P.lse[e * L.Hq + i] = -INFINITY;
-    }
-  }
+  int lens = 0, chunk = 0;
+  long long mine = 0, incl = 0, base = 0, T;
+  if (lane == 0)
+    for (int i = warp; i < kD / 2; i += NW) theta[i] = L.theta[i];
   if (tid < 2 * NW) ent[tid].gid = -1;
-  __syncthreads();
-  if (warp == 0) {                                     // exclusive sums, the total at [nc]
-    long long run = 0;
-    for (int c0 = 0; c0 < nc; c0 += 32) {
-      const long long mine = c0 + lane < nc ? prefix[c0 + lane] : 0;
-      long long incl = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long u = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += u;
-      }
-      if (c0 + lane < nc) prefix[c0 + lane] = run + incl - mine;
-      run += __shfl_sync(0xffffffffu, incl, 31);
+  if (nc == 1) {
+    bool bad = false;
+    lens = paged_len(P, lane, &bad);
+    mine = seq_tiles(L, lens);
+    incl = warp_incl_sum(mine);
+    T = __shfl_sync(0xffffffffu, incl, 31);
+    if (warp == 0) paged_idle(P, 0, lens, bad);
+  } else {
+    for (int ch = warp; ch < nc; ch += NW) {
+      bool bad = false;
+      const int n = paged_len(P, ch * 32 + lane, &bad);
+      const long long t = warp_incl_sum(seq_tiles(L, n));
+      if (lane == 31) prefix[ch] = t;
+      paged_idle(P, ch, n, bad);
     }
-    if (lane == 0) prefix[nc] = run;
+    __syncthreads();
+    if (warp == 0) {                                   // exclusive sums, the total at [nc]
+      long long run = 0;
+      for (int c0 = 0; c0 < nc; c0 += 32) {
+        const long long m = c0 + lane < nc ? prefix[c0 + lane] : 0;
+        const long long in = warp_incl_sum(m);
+        if (c0 + lane < nc) prefix[c0 + lane] = run + in - m;
+        run += __shfl_sync(0xffffffffu, in, 31);
+      }
+      if (lane == 0) prefix[nc] = run;
+    }
+    __syncthreads();
+    T = prefix[nc];
   }
-  __syncthreads();
-  const long long T = prefix[nc];
   // CTAs that take part: at least one tile per warp
   const long long PC = min((long long)gridDim.x, (T + NW - 1) / NW);
   if (blockIdx.x >= PC) return;
   const long long ct0 = blockIdx.x * T / PC, ct1 = (blockIdx.x + 1) * T / PC;
   const long long t0 = ct0 + warp * (ct1 - ct0) / NW, t1 = ct0 + (warp + 1) * (ct1 - ct0) / NW;
   const int n = (int)(t1 - t0);
+  if (nc > 1 && n > 0) {
+    int before = 0;                                    // chunks that start at or before t0
+    for (int i = lane; i < nc; i += 32) before += prefix[i] <= t0;
+    chunk = __reduce_add_sync(0xffffffffu, before) - 1;
+    base = prefix[chunk];
+    lens = paged_len(P, chunk * 32 + lane, nullptr);
+    mine = seq_tiles(L, lens);
+    incl = warp_incl_sum(mine);
+  }
+  __syncthreads();                                     // theta, ent
 
   unsigned char* ring = sm + warp * NS * Cfg::kStageB;
   const uint32_t ring_s = smem_u32(ring);
   PagedAttn<KV> A;
   if (n > 0) {
-    Cursor cc = cursor_at(P, prefix, t0), pc = cc;
-    // fill the ring: the page ids of its tiles are loaded together
+    Cursor cc = cursor_at(P, chunk, t0 - base, lens, incl, mine), pc = cc;
+    // fill the ring: the page ids of its tiles are loaded together, and the first query and its
+    // angles meanwhile
     TileDesc d[NS];
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
@@ -769,6 +814,9 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams P) {
         if (++pc.k == pc.nt) cursor_next_group(P, pc);
       }
     }
+    QueryRaw qr;
+    query_fetch<KV>(P, qr, cc.b, kv_head(L, cc.gi));
+    fill_angles(theta, ang, cc.n - 1);
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
       if (s < n) tile_issue<KV>(P, d[s], ring_s + s * Cfg::kStageB, masks + s);
@@ -779,20 +827,25 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams P) {
       nx = tile_desc(P, pc);
       if (++pc.k == pc.nt) cursor_next_group(P, pc);
     }
-    int seg_k = cc.k, ang_b = -1, slot = 0;
+    query_terms<KV>(A, qr, ang, G);
+    attn_reset<KV>(A);
+    int seg_k = cc.k, ang_b = cc.b, slot = 0;
     bool have_head = false;
     PagedEntry he;
     float sv[8][4], sv_m[2], sv_l[2], sv_mo[2];
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
       const int kvh = kv_head(L, cc.gi);
-      if (cc.k == seg_k) {                             // first tile of a group or of the range
+      if (cc.k == 0 && i > 0) {                        // first tile of a group
+        QueryRaw q2;
+        query_fetch<KV>(P, q2, cc.b, kvh);
         if (cc.b != ang_b) {
-          fill_angles(L, ang, cc.n - 1);
+          fill_angles(theta, ang, cc.n - 1);
           ang_b = cc.b;
         }
-        load_query<KV>(P, A, cc.b, kvh, ang);
+        query_terms<KV>(A, q2, ang, G);
         attn_reset<KV>(A);
+        seg_k = 0;
       }
       cp_async_wait<NS - 1>();
       __syncwarp();
@@ -802,7 +855,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams P) {
         const int pos = cc.n - 1;
         const int64_t pid = __ldg(P.C.table + (int64_t)cc.b * P.C.table_stride + (pos >> P.C.lg));
         const int64_t in = ((int64_t)kvh << P.C.lg) + (pos & ((1 << P.C.lg) - 1));
-        paged_append_row<KV>(P, cc.b, kvh, pos, pid * P.C.page_stride + in,
+        paged_append_row<KV>(P, theta, cc.b, kvh, pos, pid * P.C.page_stride + in,
                              pid * ((int64_t)L.Hkv << P.C.lg) + in, stage);
       }
       paged_tile<KV>(A, stage, mask);
@@ -821,12 +874,11 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams P) {
       if (ends || i == n - 1) {
         attn_sum<KV>(A);
         const bool starts = seg_k == 0;
-        const long long gs = t0 + i + 1 - cc.k;
         if (starts && ends) {
           attn_write<KV>(P, A, cc.b, kvh);
         } else {
           PagedEntry e;
-          e.gid = cc.b * L.Hkv + cc.gi; e.gs = gs; e.ge = gs + cc.nt; e.pad = 0;
+          e.gid = cc.b * L.Hkv + cc.gi; e.gs = t0 + i + 1 - cc.k; e.ge = e.gs + cc.nt; e.pad = 0;
           if (!starts) {
             have_head = true;
             he = e;
@@ -843,7 +895,6 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams P) {
             if (lane == 0) ent[2 * warp + 1] = e;
           }
         }
-        seg_k = 0;
         if (ends && i < n - 1) cursor_next_group(P, cc);
       }
     }
@@ -862,84 +913,120 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams P) {
   }
   __syncthreads();
 
-  // ---- the open ends of this CTA's warps, group by group in the order of the line
-  int* open_ent = reinterpret_cast<int*>(sm + S::kMisc);   // entry of the groups left open (2)
-  int n_open = 0;
-  for (int i = 0; i < 2 * NW;) {
-    const int gid = ent[i].gid;
-    if (gid < 0) { ++i; continue; }
-    int last = i;
-    for (int j = i + 1; j < 2 * NW; ++j) {
-      if (ent[j].gid == gid) last = j;
-      else if (ent[j].gid >= 0) break;
-    }
-    const long long gs = ent[i].gs, ge = ent[i].ge;
-    const bool whole = gs >= ct0 && ge <= ct1;
-    const int b = gid / L.Hkv, g = kv_head(L, gid % L.Hkv);
-    const int64_t head0 = (int64_t)b * L.Hq + (int64_t)g * G;
-    const int open_slot = gs < ct0 ? 0 : 1;
-    float* gp = P.part + (blockIdx.x * 2 + open_slot) * (int64_t)part_gmem_floats(G);
-    for (int o = tid; o < G * kD; o += NT) {
-      const int h = o >> 7, c = o & 127;
+  // ---- the open ends of this CTA's warps, merged per group (a run of entries). Every warp finds
+  // the runs; the entries' weights first, then four channels a thread.
+  PagedRun* runs = reinterpret_cast<PagedRun*>(sm + S::kRun);
+  float* ew = reinterpret_cast<float*>(sm + S::kEw);
+  float4* ml = reinterpret_cast<float4*>(sm + S::kMl);
+  auto entry_part = [&](int j) {
+    return reinterpret_cast<const float*>(sm + (j >> 1) * NS * Cfg::kStageB) +
+           (j & 1) * part_smem_floats(G);
+  };
+  int n_runs, n_open;
+  {
+    const int gid = lane < 2 * NW ? ent[lane].gid : -1;
+    const uint32_t same = __match_any_sync(0xffffffffu, gid);
+    const bool lead = gid >= 0 && __ffs(same) - 1 == lane;
+    const uint32_t leads = __ballot_sync(0xffffffffu, lead);
+    n_runs = __popc(leads);
+    bool whole = true;
+    if (lead) whole = ent[lane].gs >= ct0 && ent[lane].ge <= ct1;
+    n_open = __popc(__ballot_sync(0xffffffffu, !whole));
+    if (warp == 0 && lead)
+      runs[__popc(leads & ((1u << lane) - 1))] = {lane, same, whole, ent[lane].gs < ct0 ? 0 : 1};
+  }
+  if (n_runs == 0) return;
+  for (int o = tid; o < 2 * NW * 8; o += NT) {
+    const int j = o >> 3, h = o & 7, gid = ent[j].gid;
+    if (gid >= 0 && h < G) {
       float M = -INFINITY, MO = -INFINITY;
-      for (int j = i; j <= last; ++j)
-        if (ent[j].gid == gid) {
-          const float* part = reinterpret_cast<const float*>(sm + (j >> 1) * NS * Cfg::kStageB) +
-                              (j & 1) * part_smem_floats(G);
-          M = fmaxf(M, part[G * kPartPitch + 3 * h]);
-          MO = fmaxf(MO, part[G * kPartPitch + 3 * h + 2]);
+      int first = 2 * NW;
+#pragma unroll
+      for (int i = 2 * NW - 1; i >= 0; --i)
+        if (ent[i].gid == gid) {
+          const float* p = entry_part(i) + G * kPartPitch + 3 * h;
+          M = fmaxf(M, p[0]);
+          MO = fmaxf(MO, p[2]);
+          first = i;
         }
-      float Ls = 0.f, Ac = 0.f;
-      for (int j = i; j <= last; ++j)
-        if (ent[j].gid == gid) {
-          const float* part = reinterpret_cast<const float*>(sm + (j >> 1) * NS * Cfg::kStageB) +
-                              (j & 1) * part_smem_floats(G);
-          const float* ml = part + G * kPartPitch + 3 * h;
-          Ls += ml[1] * ex2_from(ml[0], M);
-          Ac += part[h * kPartPitch + c] * ex2_from(ml[2], MO);
-        }
-      if (whole) {
-        const float f = Ls > 0.f || Ls != Ls ? ex2_from(MO, M) / Ls : 0.f;
-        P.out[head0 * kD + o] = f2bf_rn(Ac * f);
-        if (P.lse && c == 0) P.lse[head0 + h] = (M + log2f(Ls)) * 0.6931471805599453f;
-      } else {
-        gp[o] = Ac;
-        if (c == 0) { gp[G * kD + 3 * h] = M; gp[G * kD + 3 * h + 1] = Ls; gp[G * kD + 3 * h + 2] = MO; }
+      ew[o] = ex2_from(entry_part(j)[G * kPartPitch + 3 * h + 2], MO);
+      if (j == first) {
+        float Ls = 0.f;
+        for (int i = first; i < 2 * NW; ++i)
+          if (ent[i].gid == gid) {
+            const float* p = entry_part(i) + G * kPartPitch + 3 * h;
+            Ls += p[1] * ex2_from(p[0], M);
+          }
+        ml[o] = make_float4(M, Ls, MO, Ls > 0.f || Ls != Ls ? ex2_from(MO, M) / Ls : 0.f);
       }
     }
-    if (!whole) { if (tid == 0) open_ent[n_open] = i; ++n_open; }
-    i = last + 1;
+  }
+  __syncthreads();
+  const int items = G * (kD / 4);
+  const int64_t pf = part_gmem_floats(G);
+  for (int o = tid; o < n_runs * items; o += NT) {
+    const PagedRun r = runs[o / items];
+    const int it = o % items, h = it >> 5;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (uint32_t mem = r.members; mem; mem &= mem - 1) {
+      const int j = __ffs(mem) - 1;
+      const float4 a = *reinterpret_cast<const float4*>(entry_part(j) + h * kPartPitch + 4 * (it & 31));
+      const float w = ew[8 * j + h];
+      s.x = fmaf(a.x, w, s.x); s.y = fmaf(a.y, w, s.y);
+      s.z = fmaf(a.z, w, s.z); s.w = fmaf(a.w, w, s.w);
+    }
+    const float4 st = ml[8 * r.first + h];
+    if (r.whole) {
+      const int gid = ent[r.first].gid, b = gid / L.Hkv;
+      const int64_t head0 = (int64_t)b * L.Hq + (int64_t)kv_head(L, gid - b * L.Hkv) * G;
+      uint2 w;
+      w.x = pack_bf2(s.x * st.w, s.y * st.w);
+      w.y = pack_bf2(s.z * st.w, s.w * st.w);
+      *reinterpret_cast<uint2*>(P.out + head0 * kD + 4 * it) = w;
+      if (P.lse && (it & 31) == 0) P.lse[head0 + h] = (st.x + log2f(st.y)) * 0.6931471805599453f;
+    } else {
+      float* gp = P.part + (blockIdx.x * 2 + r.slot) * pf;
+      reinterpret_cast<float4*>(gp)[it] = s;
+      if ((it & 31) == 0) {
+        gp[G * kD + 3 * h] = st.x; gp[G * kD + 3 * h + 1] = st.y; gp[G * kD + 3 * h + 2] = st.z;
+      }
+    }
   }
   if (n_open == 0) return;
-  __threadfence();
+  // ---- arrivals: a group that spans CTAs c0..c1 counts at c0's word, which wraps to zero
+  int* open_run = reinterpret_cast<int*>(sm + S::kMisc);       // [2] run, [2] last to arrive
   __syncthreads();
-  // arrivals: a group that spans CTAs c0..c1 counts at c0's word, which wraps to zero
-  if (tid < n_open) {
-    const PagedEntry e = ent[open_ent[tid]];
-    const int c0 = (int)(((e.gs + 1) * PC - 1) / T), c1 = (int)((e.ge * PC - 1) / T);
-    const uint32_t old = atomicInc(P.arrive + c0, (uint32_t)(c1 - c0));
+  if (tid == 0) {
+    __threadfence();                                   // the CTA's partials, before the arrival
+    int x = 0;
+    for (int r = 0; r < n_runs; ++r)
+      if (!runs[r].whole) {
+        const PagedEntry e = ent[runs[r].first];
+        const int c0 = (int)(((e.gs + 1) * PC - 1) / T), c1 = (int)((e.ge * PC - 1) / T);
+        open_run[x] = r;
+        open_run[2 + x] = atomicInc(P.arrive + c0, (uint32_t)(c1 - c0)) == (uint32_t)(c1 - c0);
+        ++x;
+      }
     __threadfence();
-    open_ent[2 + tid] = old == (uint32_t)(c1 - c0) ? 1 : 0;
   }
   __syncthreads();
   float* wt = reinterpret_cast<float*>(sm + S::kWt);          // [parts][8]
   float* fac = reinterpret_cast<float*>(sm + S::kMisc) + 16;  // [8]
   for (int x = 0; x < n_open; ++x) {
-    if (!open_ent[2 + x]) continue;
-    const PagedEntry e = ent[open_ent[x]];
+    if (!open_run[2 + x]) continue;
+    const PagedEntry e = ent[runs[open_run[x]].first];
     const int c0 = (int)(((e.gs + 1) * PC - 1) / T), c1 = (int)((e.ge * PC - 1) / T);
     const int np = c1 - c0 + 1;
-    const int64_t pf = part_gmem_floats(G);
     // part i: the open end of CTA c0 + i (its last group for i = 0, its first otherwise)
-    const float* base = P.part + (int64_t)c0 * 2 * pf;
-    const int b = e.gid / L.Hkv, g = kv_head(L, e.gid % L.Hkv);
-    const int64_t head0 = (int64_t)b * L.Hq + (int64_t)g * G;
+    const float* part = P.part + (int64_t)c0 * 2 * pf;
+    const int b = e.gid / L.Hkv;
+    const int64_t head0 = (int64_t)b * L.Hq + (int64_t)kv_head(L, e.gid - b * L.Hkv) * G;
     if (warp < G) {
       float M = -INFINITY, MO = -INFINITY;
       for (int i = lane; i < np; i += 32) {
-        const float* ml = base + (i * 2 + (i == 0)) * pf + G * kD + 3 * warp;
-        M = fmaxf(M, __ldcg(ml));
-        MO = fmaxf(MO, __ldcg(ml + 2));
+        const float* q = part + (i * 2 + (i == 0)) * pf + G * kD + 3 * warp;
+        M = fmaxf(M, __ldcg(q));
+        MO = fmaxf(MO, __ldcg(q + 2));
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
@@ -948,9 +1035,9 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams P) {
       }
       float Ls = 0.f;
       for (int i = lane; i < np; i += 32) {
-        const float* ml = base + (i * 2 + (i == 0)) * pf + G * kD + 3 * warp;
-        Ls += __ldcg(ml + 1) * ex2_from(__ldcg(ml), M);
-        wt[i * 8 + warp] = ex2_from(__ldcg(ml + 2), MO);
+        const float* q = part + (i * 2 + (i == 0)) * pf + G * kD + 3 * warp;
+        Ls += __ldcg(q + 1) * ex2_from(__ldcg(q), M);
+        wt[i * 8 + warp] = ex2_from(__ldcg(q + 2), MO);
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) Ls += __shfl_xor_sync(0xffffffffu, Ls, o);
@@ -960,16 +1047,17 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams P) {
       }
     }
     __syncthreads();
-    // four channels a thread; where G is small, thread teams share out the parts
-    const int items = G * (kD / 4), teams = NT / items;        // 1, 2, 4 or 8 teams
-    const int team = tid / items, it = tid % items, h = it >> 5;
+    // four channels a thread; where G is small, teams of threads share out the parts
+    const int teams = NT / items, team = tid / items, it = tid - team * items, h = it >> 5;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (team < teams) {
 #pragma unroll 4
-    for (int i = team; i < np; i += teams) {
-      const float4 a = __ldcg(reinterpret_cast<const float4*>(base + (i * 2 + (i == 0)) * pf) + it);
-      const float w = wt[i * 8 + h];
-      s.x = fmaf(a.x, w, s.x); s.y = fmaf(a.y, w, s.y);
-      s.z = fmaf(a.z, w, s.z); s.w = fmaf(a.w, w, s.w);
+      for (int i = team; i < np; i += teams) {
+        const float4 a = __ldcg(reinterpret_cast<const float4*>(part + (i * 2 + (i == 0)) * pf) + it);
+        const float w = wt[i * 8 + h];
+        s.x = fmaf(a.x, w, s.x); s.y = fmaf(a.y, w, s.y);
+        s.z = fmaf(a.z, w, s.z); s.w = fmaf(a.w, w, s.w);
+      }
     }
     float4* red = reinterpret_cast<float4*>(sm);
     red[tid] = s;
