@@ -621,6 +621,7 @@ int paged_decode_impl(const rtp_layer_desc* desc, const rtp_paged_cache* cache,
   P.status = static_cast<int*>(ws);
   P.arrive = at<uint32_t>(ws, 256);
   P.part = at<float>(ws, kPagedCtrlBytes);
+  P.head = P.part + (size_t)2 * kPagedMaxCTAs * cta_part_floats(P.L.G);
   cudaStream_t st = (cudaStream_t)stream;
   if (cache->kv_type == RTP_KV_BF16)
     return append ? launch_paged<kKvBf16, true>(P, di, st) : launch_paged<kKvBf16, false>(P, di, st);
@@ -635,7 +636,7 @@ size_t rtp_paged_workspace_bytes(const rtp_layer_desc* desc) {
   LayerShape L;
   if (check_desc(desc, L) != RTP_OK) return 0;
   return RTP_PAGED_CTRL_BYTES +
-         size_t(2) * kPagedMaxCTAs * part_gmem_floats(L.G) * sizeof(float);
+         paged_part_floats(L.G) * sizeof(float);
 }
 
 int rtp_paged_workspace_init(void* ws, size_t ws_bytes, rtp_stream_t stream) {

@@ -45,28 +45,36 @@ struct PagedDecodeParams {
   float* lse;
   int* status;
   uint32_t* arrive;
-  float* part;
+  float *part, *head;            // [CTAs][2] partials of CTAs, [CTAs][16] of warps
 };
 
 template <int KV> struct PagedCfg;
-// 8 warps with three 8 KB tiles each: 192 KB of copies in the ring
 template <> struct PagedCfg<kKvBf16> {
   static constexpr int kWarps = 8, kStages = 3, kRowB = 256, kTerms = 3;
   static constexpr int kStageB = 16 * 512;
 };
 template <> struct PagedCfg<kKvE4m3> {
-  static constexpr int kWarps = 12, kStages = 4, kRowB = 128, kTerms = 2;
+  static constexpr int kWarps = 16, kStages = 3, kRowB = 128, kTerms = 2;
   static constexpr int kStageB = 16 * 256 + 128;
 };
 
-// floats of a partial in shared memory (rows of 132: the accumulators' lanes hit all banks) and
-// in the workspace
+
+constexpr int kPagedMaxWarps = 16;
+// Tiles' worth of a group's fixed cost (query, angles, output) in the split of the line
+constexpr int kSetup = 3;
+static_assert(kSetup > 0, "an empty sequence at the end of the line is divided by it");
+
+// floats of a warp's partial (rows of 132: the accumulators' lanes hit all banks) and of a CTA's
 constexpr int kPartPitch = 132;
-__host__ __device__ constexpr int part_smem_floats(int G) { return G * kPartPitch + 32; }
-__host__ __device__ constexpr int part_gmem_floats(int G) { return G * kD + 32; }
+__host__ __device__ constexpr int warp_part_floats(int G) { return G * kPartPitch + 32; }
+__host__ __device__ constexpr int cta_part_floats(int G) { return G * kD + 32; }
+__host__ __device__ constexpr size_t paged_part_floats(int G) {
+  return (size_t)2 * kPagedMaxCTAs * cta_part_floats(G) +
+         (size_t)kPagedMaxCTAs * kPagedMaxWarps * warp_part_floats(G);
+}
 
 struct PagedEntry {              // an open end of a warp's range
-  long long gs, ge;              // tiles of its group
+  long long gs, ge;              // its group on the line: first tile, end
   int gid;                       // sequence * Hkv + position of the KV head in the group order; -1: none
   int pad;
 };
@@ -75,21 +83,21 @@ template <int KV>
 struct PagedSmem {
   using Cfg = PagedCfg<KV>;
   static constexpr int kEntries = 2 * Cfg::kWarps;
+  static_assert(kEntries <= 32, "a warp's lanes stand for the entries");
   static constexpr int kRing = Cfg::kWarps * Cfg::kStages * Cfg::kStageB;
   static constexpr int kTheta = kRing;                             // [64] doubles
   static constexpr int kAng = kTheta + 64 * 8;                     // [warps][64] (cos, sin)
   static constexpr int kMask = kAng + Cfg::kWarps * 64 * 8;        // [warps][8] row masks
   static constexpr int kEnt = kMask + Cfg::kWarps * 8 * 4;
-  static constexpr int kRun = kEnt + kEntries * (int)sizeof(PagedEntry);   // [entries] PagedRun
-  static constexpr int kEw = kRun + kEntries * 16;                 // [entries][8] weights
-  static constexpr int kMl = kEw + kEntries * 8 * 4;               // [entries][8] (M, L, MO, factor)
-  static constexpr int kPrefix = kMl + kEntries * 8 * 16;
-  static constexpr int kMisc = kPrefix + 130 * 8;
+  static constexpr int kList = kEnt + kEntries * (int)sizeof(PagedEntry);  // [warps][32] bytes
+  static constexpr int kPrefix = kList + Cfg::kWarps * 32;         // [129] line, [129] sequences
+  static constexpr int kMisc = kPrefix + 130 * 8 + 130 * 8;
   static constexpr int kWt = kMisc + 256;                          // [160][8] weights of a merge
   static constexpr int kBytes = kWt + kPagedMaxCTAs * 8 * 4;
+  // a drained ring: two partials, then [entries][8] weights of a merge
+  static constexpr int kEw = 2 * warp_part_floats(8) * 4;
+  static_assert(kEw + kEntries * 8 * 4 <= Cfg::kStages * Cfg::kStageB, "partials fit the ring");
 };
-// entries of one group in a CTA: the first, all of them (bits), whether the group is complete
-struct PagedRun { int first; uint32_t members; int whole, slot; };
 
 // ------------------------------------------------------------------ conversions and products
 
@@ -176,9 +184,11 @@ __device__ __forceinline__ LocalTiles local_tiles(const LayerShape& L, int n) {
   t.nt = t.ns + tr - wt;
   return t;
 }
-__device__ __forceinline__ long long seq_tiles(const LayerShape& L, int n) {
+// Length of a sequence on the line: a group is kSetup places without a tile, then its tiles.
+__device__ __forceinline__ long long seq_places(const LayerShape& L, int n) {
   if (n <= 0) return 0;
-  return (long long)L.n_ret * ((n + 15) >> 4) + (long long)L.n_loc * local_tiles(L, n).nt;
+  return (long long)L.n_ret * (((n + 15) >> 4) + kSetup) +
+         (long long)L.n_loc * (local_tiles(L, n).nt + kSetup);
 }
 
 // A place on the line. Sequences are in batch order; in a sequence the retrieval KV heads come
@@ -211,25 +221,38 @@ __device__ __forceinline__ void cursor_next_group(const PagedDecodeParams& P, Cu
   }
   cursor_group(P.L, c);
 }
-// The cursor of the tile that is rel tiles after the start of a chunk of 32 sequences; lens: this
-// lane's length of the chunk, incl and mine: its tiles with and without the lanes before.
-__device__ __forceinline__ Cursor cursor_at(const PagedDecodeParams& P, int chunk, long long rel,
-                                            int lens, long long incl, long long mine) {
+// The cursor of the first tile at or after a place of the line, rel places after the start of a
+// chunk of 32 sequences. lens: this lane's length of the chunk; incl and mine: its places with
+// and without the lanes before. *before: tiles of the line before that one, where seqs non-empty
+// sequences lie before the chunk; *first: its place.
+__device__ __forceinline__ Cursor cursor_at(const PagedDecodeParams& P, int chunk, long long place,
+                                            long long base, int seqs, int lens, long long incl,
+                                            long long mine, long long* before,
+                                            long long* first) {
   Cursor c;
+  const long long rel = place - base;
   c.lens = lens;
-  const int j = __popc(__ballot_sync(0xffffffffu, incl <= rel));
+  // (the end of the line, past the last sequence, has no tile; its count of tiles is right)
+  const uint32_t done = __ballot_sync(0xffffffffu, incl <= rel);
+  const uint32_t live = __ballot_sync(0xffffffffu, lens > 0);
+  const int j = min(__popc(done), 31);
   c.b = chunk * 32 + j;
   c.n = __shfl_sync(0xffffffffu, lens, j);
   const int in_seq = (int)(rel - __shfl_sync(0xffffffffu, incl - mine, j));
-  const int tr = (c.n + 15) >> 4;
+  const int tr = ((c.n + 15) >> 4) + kSetup;
+  int k;
   if (in_seq < P.L.n_ret * tr) {
     c.gi = in_seq / tr;
-    c.k = in_seq - c.gi * tr;
+    k = in_seq - c.gi * tr;
   } else {
-    const int u = in_seq - P.L.n_ret * tr, tl = local_tiles(P.L, c.n).nt;
+    const int u = in_seq - P.L.n_ret * tr, tl = local_tiles(P.L, c.n).nt + kSetup;
     c.gi = P.L.n_ret + u / tl;
-    c.k = u % tl;
+    k = u % tl;
   }
+  const long long groups = (long long)(seqs + __popc(live & ((1u << j) - 1))) * P.L.Hkv + c.gi;
+  *before = place - groups * kSetup - min(k, kSetup);
+  *first = place + max(kSetup - k, 0);
+  c.k = max(k - kSetup, 0);
   cursor_group(P.L, c);
   return c;
 }
@@ -241,6 +264,37 @@ __device__ __forceinline__ long long warp_incl_sum(long long x) {
     if (lane >= o) x += u;
   }
   return x;
+}
+
+// The line cut into n <= 160 ranges, the first `extra` of them one place longer. Plain 64-bit
+// divisions cost about 500 cycles each here; there is one left, for lines beyond 2^32 places.
+struct LineSplit {
+  long long each, T;
+  int n, extra;
+  float inv, inv1;
+};
+__device__ __forceinline__ LineSplit split_line(long long T, int n) {
+  LineSplit s;
+  s.T = T;
+  s.n = n;
+  s.each = T >> 32 ? T / n : (long long)((uint32_t)T / (uint32_t)n);
+  s.extra = (int)(T - s.each * n);
+  s.inv = 1.f / (float)s.each;
+  s.inv1 = 1.f / (float)(s.each + 1);
+  return s;
+}
+__device__ __forceinline__ long long range_start(const LineSplit& s, int i) {
+  return s.each * i + min(i, s.extra);
+}
+// The range that holds a place: the quotient is below 160, so its single-precision estimate is
+// off by one at most.
+__device__ __forceinline__ int range_of(const LineSplit& s, long long place) {
+  int i = min((int)((float)place * s.inv1), s.n - 1);
+  if (i >= s.extra)
+    i = min(s.extra + (int)((float)(place - s.extra * (s.each + 1)) * s.inv), s.n - 1);
+  if (range_start(s, i) > place) --i;
+  if (i + 1 < s.n && range_start(s, i + 1) <= place) ++i;
+  return i;
 }
 
 struct TileDesc { int pid, row; uint32_t mask; };   // page, row in the page block, rows attended
@@ -745,57 +799,78 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams P) {
   float2* ang = reinterpret_cast<float2*>(sm + S::kAng) + warp * 64;
   uint32_t* masks = reinterpret_cast<uint32_t*>(sm + S::kMask) + warp * 8;
 
-  // ---- the line: tiles before each 32 sequences, and in all. Up to 32 sequences: every warp
+  // ---- the line: places before each 32 sequences, and in all. Up to 32 sequences: every warp
   // makes the sums itself.
   const int nc = (L.B + 31) >> 5;
-  int lens = 0, chunk = 0;
+  long long* seqs_before = prefix + 130;
+  int lens = 0, chunk = 0, seqs = 0;
   long long mine = 0, incl = 0, base = 0, T;
-  if (lane == 0)
-    for (int i = warp; i < kD / 2; i += NW) theta[i] = L.theta[i];
   if (tid < 2 * NW) ent[tid].gid = -1;
+  bool bad = false;
+  if (nc == 1) lens = paged_len(P, lane, &bad);
+  if (lane == 0) {                                     // while the lengths are on their way
+#pragma unroll
+    for (int i = 0; i < kD / 2 / NW; ++i) theta[warp * (kD / 2 / NW) + i] = L.theta[warp * (kD / 2 / NW) + i];
+  }
   if (nc == 1) {
-    bool bad = false;
-    lens = paged_len(P, lane, &bad);
-    mine = seq_tiles(L, lens);
+    mine = seq_places(L, lens);
     incl = warp_incl_sum(mine);
     T = __shfl_sync(0xffffffffu, incl, 31);
     if (warp == 0) paged_idle(P, 0, lens, bad);
   } else {
     for (int ch = warp; ch < nc; ch += NW) {
-      bool bad = false;
+      bad = false;
       const int n = paged_len(P, ch * 32 + lane, &bad);
-      const long long t = warp_incl_sum(seq_tiles(L, n));
-      if (lane == 31) prefix[ch] = t;
+      const long long t = warp_incl_sum(seq_places(L, n));
+      const uint32_t live = __ballot_sync(0xffffffffu, n > 0);
+      if (lane == 31) { prefix[ch] = t; seqs_before[ch] = __popc(live); }
       paged_idle(P, ch, n, bad);
     }
     __syncthreads();
-    if (warp == 0) {                                   // exclusive sums, the total at [nc]
+    if (warp < 2) {                                    // exclusive sums, the total at [nc]
+      long long* x = warp ? seqs_before : prefix;
       long long run = 0;
       for (int c0 = 0; c0 < nc; c0 += 32) {
-        const long long m = c0 + lane < nc ? prefix[c0 + lane] : 0;
+        const long long m = c0 + lane < nc ? x[c0 + lane] : 0;
         const long long in = warp_incl_sum(m);
-        if (c0 + lane < nc) prefix[c0 + lane] = run + in - m;
+        if (c0 + lane < nc) x[c0 + lane] = run + in - m;
         run += __shfl_sync(0xffffffffu, in, 31);
       }
-      if (lane == 0) prefix[nc] = run;
+      if (lane == 0) x[nc] = run;
     }
     __syncthreads();
     T = prefix[nc];
   }
-  // CTAs that take part: at least one tile per warp
-  const long long PC = min((long long)gridDim.x, (T + NW - 1) / NW);
-  if (blockIdx.x >= PC) return;
-  const long long ct0 = blockIdx.x * T / PC, ct1 = (blockIdx.x + 1) * T / PC;
-  const long long t0 = ct0 + warp * (ct1 - ct0) / NW, t1 = ct0 + (warp + 1) * (ct1 - ct0) / NW;
-  const int n = (int)(t1 - t0);
-  if (nc > 1 && n > 0) {
-    int before = 0;                                    // chunks that start at or before t0
-    for (int i = lane; i < nc; i += 32) before += prefix[i] <= t0;
-    chunk = __reduce_add_sync(0xffffffffu, before) - 1;
-    base = prefix[chunk];
-    lens = paged_len(P, chunk * 32 + lane, nullptr);
-    mine = seq_tiles(L, lens);
-    incl = warp_incl_sum(mine);
+  // CTAs that take part: at least one place per warp
+  if (T == 0) return;
+  const LineSplit split = split_line(T, T >= (long long)gridDim.x * NW ? (int)gridDim.x
+                                                                       : ((int)T + NW - 1) / NW);
+  if (blockIdx.x >= split.n) return;
+  const long long ct0 = range_start(split, blockIdx.x), ct1 = range_start(split, blockIdx.x + 1);
+  const int len = (int)(ct1 - ct0);                    // below 2^31: a sequence has 2^26 places at most
+  const long long p0 = ct0 + (int)((long long)warp * len / NW);
+  const long long p1 = ct0 + (int)((long long)(warp + 1) * len / NW);
+  Cursor cc;
+  long long line;                                      // place of the tile at cc
+  int n = 0;                                           // tiles of this warp
+  {
+    long long tiles[2];
+#pragma unroll
+    for (int e = 1; e >= 0; --e) {                     // the end, then the start (which stays in cc)
+      const long long p = e ? p1 : p0;
+      if (nc > 1) {
+        int before = 0;                                // chunks that start at or before p
+        for (int i = lane; i < nc; i += 32) before += prefix[i] <= p;
+        chunk = __reduce_add_sync(0xffffffffu, before) - 1;
+        base = prefix[chunk];
+        seqs = (int)seqs_before[chunk];
+        lens = paged_len(P, chunk * 32 + lane, nullptr);
+        mine = seq_places(L, lens);
+        incl = warp_incl_sum(mine);
+      }
+      cc = cursor_at(P, chunk, p, base, seqs, lens, incl, mine, &tiles[e], &line);
+    }
+    n = (int)(tiles[1] - tiles[0]);
   }
   __syncthreads();                                     // theta, ent
 
@@ -803,7 +878,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams P) {
   const uint32_t ring_s = smem_u32(ring);
   PagedAttn<KV> A;
   if (n > 0) {
-    Cursor cc = cursor_at(P, chunk, t0 - base, lens, incl, mine), pc = cc;
+    Cursor pc = cc;
     // fill the ring: the page ids of its tiles are loaded together, and the first query and its
     // angles meanwhile
     TileDesc d[NS];
@@ -830,9 +905,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams P) {
     query_terms<KV>(A, qr, ang, G);
     attn_reset<KV>(A);
     int seg_k = cc.k, ang_b = cc.b, slot = 0;
-    bool have_head = false;
-    PagedEntry he;
-    float sv[8][4], sv_m[2], sv_l[2], sv_mo[2];
+    bool has_head = false;
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
       const int kvh = kv_head(L, cc.gi);
@@ -870,6 +943,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams P) {
       cp_async_commit();
       if (++slot == NS) slot = 0;
       ++cc.k;
+      ++line;
       const bool ends = cc.k == cc.nt;
       if (ends || i == n - 1) {
         attn_sum<KV>(A);
@@ -877,167 +951,197 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams P) {
         if (starts && ends) {
           attn_write<KV>(P, A, cc.b, kvh);
         } else {
-          PagedEntry e;
-          e.gid = cc.b * L.Hkv + cc.gi; e.gs = t0 + i + 1 - cc.k; e.ge = e.gs + cc.nt; e.pad = 0;
-          if (!starts) {
-            have_head = true;
-            he = e;
-#pragma unroll
-            for (int u = 0; u < 8; ++u)
-#pragma unroll
-              for (int w = 0; w < 4; ++w) sv[u][w] = A.acc[u][w];
-#pragma unroll
-            for (int w = 0; w < 2; ++w) { sv_m[w] = A.m[w]; sv_l[w] = A.l[w]; sv_mo[w] = A.mo[w]; }
-          } else {                                     // only at the end of the range
+          // an open end: to the drained ring, or, where tiles of other groups follow and the ring
+          // is in use, to the workspace for now (then it is of a group that an earlier warp began)
+          float* dst = reinterpret_cast<float*>(ring) + (starts ? warp_part_floats(G) : 0);
+          if (i < n - 1) {
+            dst = P.head + (int64_t)(blockIdx.x * NW + warp) * warp_part_floats(G);
+            has_head = true;
+          } else {
             cp_async_wait<0>();
             __syncwarp();
-            attn_store<KV>(A, reinterpret_cast<float*>(ring) + part_smem_floats(G), G);
-            if (lane == 0) ent[2 * warp + 1] = e;
+          }
+          attn_store<KV>(A, dst, G);
+          if (lane == 0) {
+            PagedEntry e;
+            e.gid = cc.b * L.Hkv + cc.gi;
+            e.ge = line + (cc.nt - cc.k);
+            e.gs = e.ge - cc.nt;
+            e.pad = 0;
+            ent[2 * warp + (starts ? 1 : 0)] = e;
           }
         }
-        if (ends && i < n - 1) cursor_next_group(P, cc);
+        if (ends && i < n - 1) {
+          cursor_next_group(P, cc);
+          line += kSetup;
+        }
       }
     }
     cp_async_wait<0>();
     __syncwarp();
-    if (have_head) {
-#pragma unroll
-      for (int u = 0; u < 8; ++u)
-#pragma unroll
-        for (int w = 0; w < 4; ++w) A.acc[u][w] = sv[u][w];
-#pragma unroll
-      for (int w = 0; w < 2; ++w) { A.m[w] = sv_m[w]; A.l[w] = sv_l[w]; A.mo[w] = sv_mo[w]; }
-      attn_store<KV>(A, reinterpret_cast<float*>(ring), G);
-      if (lane == 0) ent[2 * warp] = he;
+    if (has_head) {
+      const float4* src = reinterpret_cast<const float4*>(
+          P.head + (int64_t)(blockIdx.x * NW + warp) * warp_part_floats(G));
+#pragma unroll 9
+      for (int i = lane; i < warp_part_floats(G) / 4; i += 32)
+        reinterpret_cast<float4*>(ring)[i] = src[i];
     }
   }
   __syncthreads();
 
-  // ---- the open ends of this CTA's warps, merged per group (a run of entries). Every warp finds
-  // the runs; the entries' weights first, then four channels a thread.
-  PagedRun* runs = reinterpret_cast<PagedRun*>(sm + S::kRun);
-  float* ew = reinterpret_cast<float*>(sm + S::kEw);
-  float4* ml = reinterpret_cast<float4*>(sm + S::kMl);
-  auto entry_part = [&](int j) {
-    return reinterpret_cast<const float*>(sm + (j >> 1) * NS * Cfg::kStageB) +
-           (j & 1) * part_smem_floats(G);
-  };
-  int n_runs, n_open;
+  // ---- the open ends of this CTA's warps: the entries of a group (a run) are merged in the order
+  // of the line, its heads shared out among NW / runs warps
+  int open_run[2] = {-1, -1};                          // first entry of the groups left open
   {
+    float* ew = reinterpret_cast<float*>(ring + S::kEw);
+    unsigned char* list = sm + S::kList + warp * 32;
     const int gid = lane < 2 * NW ? ent[lane].gid : -1;
-    const uint32_t same = __match_any_sync(0xffffffffu, gid);
-    const bool lead = gid >= 0 && __ffs(same) - 1 == lane;
-    const uint32_t leads = __ballot_sync(0xffffffffu, lead);
-    n_runs = __popc(leads);
-    bool whole = true;
-    if (lead) whole = ent[lane].gs >= ct0 && ent[lane].ge <= ct1;
-    n_open = __popc(__ballot_sync(0xffffffffu, !whole));
-    if (warp == 0 && lead)
-      runs[__popc(leads & ((1u << lane) - 1))] = {lane, same, whole, ent[lane].gs < ct0 ? 0 : 1};
-  }
-  if (n_runs == 0) return;
-  for (int o = tid; o < 2 * NW * 8; o += NT) {
-    const int j = o >> 3, h = o & 7, gid = ent[j].gid;
-    if (gid >= 0 && h < G) {
-      float M = -INFINITY, MO = -INFINITY;
-      int first = 2 * NW;
+    uint32_t same = 0;                                 // (a match instruction took 1000 cycles a value)
 #pragma unroll
-      for (int i = 2 * NW - 1; i >= 0; --i)
-        if (ent[i].gid == gid) {
-          const float* p = entry_part(i) + G * kPartPitch + 3 * h;
-          M = fmaxf(M, p[0]);
-          MO = fmaxf(MO, p[2]);
-          first = i;
+    for (int i = 0; i < 2 * NW; ++i) same |= (uint32_t)(__shfl_sync(0xffffffffu, gid, i) == gid) << i;
+    const bool lead = gid >= 0 && __ffs(same) - 1 == lane;
+    uint32_t leads = __ballot_sync(0xffffffffu, lead);
+    const uint32_t left = __ballot_sync(0xffffffffu, lead && ent[lane & (2 * NW - 1)].gs < ct0);
+    const uint32_t right = __ballot_sync(0xffffffffu, lead && ent[lane & (2 * NW - 1)].ge > ct1);
+    if (left) open_run[0] = __ffs(left) - 1;
+    if (right & ~left) open_run[1] = __ffs(right & ~left) - 1;
+    const int n_runs = __popc(leads);
+    const int share = max(1, NW / max(n_runs, 1));     // warps of a run
+    const int teams = NW / share, team = warp / share;
+    for (int r = 0; leads; ++r, leads &= leads - 1) {
+      if (r % teams != team) continue;
+      const int first = __ffs(leads) - 1;
+      const uint32_t members = __shfl_sync(0xffffffffu, same, first);
+      const int cnt = __popc(members);
+      __syncwarp();
+      if ((members >> lane) & 1u) list[__popc(members & ((1u << lane) - 1))] = lane;
+      __syncwarp();
+      auto part_of = [&](int i) {
+        const int j = list[i];
+        return reinterpret_cast<const float*>(sm + (j >> 1) * NS * Cfg::kStageB) +
+               (j & 1) * warp_part_floats(G);
+      };
+      // head lane % 8 over entries lane / 8, lane / 8 + 4, ...
+      const int h8 = lane & 7;
+      float M = -INFINITY, MO = -INFINITY, Ls = 0.f;
+      if (h8 < G)
+        for (int i = lane >> 3; i < cnt; i += 4) {
+          const float* q = part_of(i) + G * kPartPitch + 3 * h8;
+          M = fmaxf(M, q[0]);
+          MO = fmaxf(MO, q[2]);
         }
-      ew[o] = ex2_from(entry_part(j)[G * kPartPitch + 3 * h + 2], MO);
-      if (j == first) {
-        float Ls = 0.f;
-        for (int i = first; i < 2 * NW; ++i)
-          if (ent[i].gid == gid) {
-            const float* p = entry_part(i) + G * kPartPitch + 3 * h;
-            Ls += p[1] * ex2_from(p[0], M);
+#pragma unroll
+      for (int o = 8; o < 32; o <<= 1) {
+        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        MO = fmaxf(MO, __shfl_xor_sync(0xffffffffu, MO, o));
+      }
+      if (h8 < G)
+        for (int i = lane >> 3; i < cnt; i += 4) {
+          const float* q = part_of(i) + G * kPartPitch + 3 * h8;
+          Ls += q[1] * ex2_from(q[0], M);
+          ew[i * 8 + h8] = ex2_from(q[2], MO);
+        }
+#pragma unroll
+      for (int o = 8; o < 32; o <<= 1) Ls += __shfl_xor_sync(0xffffffffu, Ls, o);
+      __syncwarp();
+      const float f = Ls > 0.f || Ls != Ls ? ex2_from(MO, M) / Ls : 0.f;
+      const bool whole = first != open_run[0] && first != open_run[1];
+      const int gd = ent[first].gid, b = gd / L.Hkv;
+      const int64_t head0 = (int64_t)b * L.Hq + (int64_t)kv_head(L, gd - b * L.Hkv) * G;
+      float* gp = P.part + (int64_t)(blockIdx.x * 2 + (first == open_run[0] ? 0 : 1)) * cta_part_floats(G);
+      for (int h = warp % share; h < G; h += share) {
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int i = 0; i < cnt; ++i) {
+          const float4 a = *reinterpret_cast<const float4*>(part_of(i) + h * kPartPitch + 4 * lane);
+          const float w = ew[i * 8 + h];
+          s.x = fmaf(a.x, w, s.x); s.y = fmaf(a.y, w, s.y);
+          s.z = fmaf(a.z, w, s.z); s.w = fmaf(a.w, w, s.w);
+        }
+        if (whole) {
+          const float fh = __shfl_sync(0xffffffffu, f, h);
+          uint2 w;
+          w.x = pack_bf2(s.x * fh, s.y * fh);
+          w.y = pack_bf2(s.z * fh, s.w * fh);
+          *reinterpret_cast<uint2*>(P.out + (head0 + h) * kD + 4 * lane) = w;
+          if (P.lse && lane == h) P.lse[head0 + h] = (M + log2f(Ls)) * 0.6931471805599453f;
+        } else {
+          *reinterpret_cast<float4*>(gp + h * kD + 4 * lane) = s;
+          if (lane == h) {
+            gp[G * kD + 3 * h] = M; gp[G * kD + 3 * h + 1] = Ls; gp[G * kD + 3 * h + 2] = MO;
           }
-        ml[o] = make_float4(M, Ls, MO, Ls > 0.f || Ls != Ls ? ex2_from(MO, M) / Ls : 0.f);
+        }
       }
     }
   }
+  if (open_run[0] < 0 && open_run[1] < 0) return;
   __syncthreads();
-  const int items = G * (kD / 4);
-  const int64_t pf = part_gmem_floats(G);
-  for (int o = tid; o < n_runs * items; o += NT) {
-    const PagedRun r = runs[o / items];
-    const int it = o % items, h = it >> 5;
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (uint32_t mem = r.members; mem; mem &= mem - 1) {
-      const int j = __ffs(mem) - 1;
-      const float4 a = *reinterpret_cast<const float4*>(entry_part(j) + h * kPartPitch + 4 * (it & 31));
-      const float w = ew[8 * j + h];
-      s.x = fmaf(a.x, w, s.x); s.y = fmaf(a.y, w, s.y);
-      s.z = fmaf(a.z, w, s.z); s.w = fmaf(a.w, w, s.w);
+  // a group that spans CTAs c0..c1 counts its arrivals at c0's word, which wraps to zero
+  int* finish = reinterpret_cast<int*>(sm + S::kMisc);
+  if (tid < 2) {
+    const int first = tid ? open_run[1] : open_run[0];
+    int last = 0;
+    if (first >= 0) {
+      const PagedEntry e = ent[first];
+      const int c0 = range_of(split, e.gs), c1 = range_of(split, e.ge - 1);
+      __threadfence();                                 // the CTA's partial, before the arrival
+      last = atomicInc(P.arrive + c0, (uint32_t)(c1 - c0)) == (uint32_t)(c1 - c0);
+      __threadfence();
     }
-    const float4 st = ml[8 * r.first + h];
-    if (r.whole) {
-      const int gid = ent[r.first].gid, b = gid / L.Hkv;
-      const int64_t head0 = (int64_t)b * L.Hq + (int64_t)kv_head(L, gid - b * L.Hkv) * G;
-      uint2 w;
-      w.x = pack_bf2(s.x * st.w, s.y * st.w);
-      w.y = pack_bf2(s.z * st.w, s.w * st.w);
-      *reinterpret_cast<uint2*>(P.out + head0 * kD + 4 * it) = w;
-      if (P.lse && (it & 31) == 0) P.lse[head0 + h] = (st.x + log2f(st.y)) * 0.6931471805599453f;
-    } else {
-      float* gp = P.part + (blockIdx.x * 2 + r.slot) * pf;
-      reinterpret_cast<float4*>(gp)[it] = s;
-      if ((it & 31) == 0) {
-        gp[G * kD + 3 * h] = st.x; gp[G * kD + 3 * h + 1] = st.y; gp[G * kD + 3 * h + 2] = st.z;
-      }
-    }
-  }
-  if (n_open == 0) return;
-  // ---- arrivals: a group that spans CTAs c0..c1 counts at c0's word, which wraps to zero
-  int* open_run = reinterpret_cast<int*>(sm + S::kMisc);       // [2] run, [2] last to arrive
-  __syncthreads();
-  if (tid == 0) {
-    __threadfence();                                   // the CTA's partials, before the arrival
-    int x = 0;
-    for (int r = 0; r < n_runs; ++r)
-      if (!runs[r].whole) {
-        const PagedEntry e = ent[runs[r].first];
-        const int c0 = (int)(((e.gs + 1) * PC - 1) / T), c1 = (int)((e.ge * PC - 1) / T);
-        open_run[x] = r;
-        open_run[2 + x] = atomicInc(P.arrive + c0, (uint32_t)(c1 - c0)) == (uint32_t)(c1 - c0);
-        ++x;
-      }
-    __threadfence();
+    finish[tid] = last;
   }
   __syncthreads();
+
+  // ---- groups at which this CTA was the last to arrive
   float* wt = reinterpret_cast<float*>(sm + S::kWt);          // [parts][8]
   float* fac = reinterpret_cast<float*>(sm + S::kMisc) + 16;  // [8]
-  for (int x = 0; x < n_open; ++x) {
-    if (!open_run[2 + x]) continue;
-    const PagedEntry e = ent[runs[open_run[x]].first];
-    const int c0 = (int)(((e.gs + 1) * PC - 1) / T), c1 = (int)((e.ge * PC - 1) / T);
-    const int np = c1 - c0 + 1;
+  const int items = G * (kD / 4);
+  const int64_t pf = cta_part_floats(G);
+  for (int x = 0; x < 2; ++x) {
+    if (!finish[x]) continue;
+    const PagedEntry e = ent[x ? open_run[1] : open_run[0]];
+    const int c0 = range_of(split, e.gs), np = range_of(split, e.ge - 1) - c0 + 1;
     // part i: the open end of CTA c0 + i (its last group for i = 0, its first otherwise)
     const float* part = P.part + (int64_t)c0 * 2 * pf;
     const int b = e.gid / L.Hkv;
     const int64_t head0 = (int64_t)b * L.Hq + (int64_t)kv_head(L, e.gid - b * L.Hkv) * G;
+    // four channels a thread; where G is small, teams of threads share out the parts. The first
+    // parts are on their way while the weights are made.
+    constexpr int kAhead = 4;
+    const int teams = NT / items, team = tid / items, it = tid - team * items, h = it >> 5;
+    float4 ahead[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int i = team + u * teams;
+      ahead[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (team < teams && i < np)
+        ahead[u] = __ldcg(reinterpret_cast<const float4*>(part + (i * 2 + (i == 0)) * pf) + it);
+    }
     if (warp < G) {
-      float M = -INFINITY, MO = -INFINITY;
-      for (int i = lane; i < np; i += 32) {
+      float m[kPagedMaxCTAs / 32], l[kPagedMaxCTAs / 32], mo[kPagedMaxCTAs / 32];
+      float M = -INFINITY, MO = -INFINITY, Ls = 0.f;
+#pragma unroll
+      for (int u = 0; u < kPagedMaxCTAs / 32; ++u) {
+        const int i = lane + 32 * u;
         const float* q = part + (i * 2 + (i == 0)) * pf + G * kD + 3 * warp;
-        M = fmaxf(M, __ldcg(q));
-        MO = fmaxf(MO, __ldcg(q + 2));
+        m[u] = i < np ? __ldcg(q) : -INFINITY;
+        l[u] = i < np ? __ldcg(q + 1) : 0.f;
+        mo[u] = i < np ? __ldcg(q + 2) : -INFINITY;
       }
+#pragma unroll
+      for (int u = 0; u < kPagedMaxCTAs / 32; ++u) { M = fmaxf(M, m[u]); MO = fmaxf(MO, mo[u]); }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
         M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
         MO = fmaxf(MO, __shfl_xor_sync(0xffffffffu, MO, o));
       }
-      float Ls = 0.f;
-      for (int i = lane; i < np; i += 32) {
-        const float* q = part + (i * 2 + (i == 0)) * pf + G * kD + 3 * warp;
-        Ls += __ldcg(q + 1) * ex2_from(__ldcg(q), M);
-        wt[i * 8 + warp] = ex2_from(__ldcg(q + 2), MO);
+#pragma unroll
+      for (int u = 0; u < kPagedMaxCTAs / 32; ++u) {
+        const int i = lane + 32 * u;
+        if (i < np) {
+          Ls += l[u] * ex2_from(m[u], M);
+          wt[i * 8 + warp] = ex2_from(mo[u], MO);
+        }
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) Ls += __shfl_xor_sync(0xffffffffu, Ls, o);
@@ -1047,17 +1151,19 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams P) {
       }
     }
     __syncthreads();
-    // four channels a thread; where G is small, teams of threads share out the parts
-    const int teams = NT / items, team = tid / items, it = tid - team * items, h = it >> 5;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](const float4& a, int i) {
+      const float w = wt[i * 8 + h];
+      s.x = fmaf(a.x, w, s.x); s.y = fmaf(a.y, w, s.y);
+      s.z = fmaf(a.z, w, s.z); s.w = fmaf(a.w, w, s.w);
+    };
     if (team < teams) {
-#pragma unroll 4
-      for (int i = team; i < np; i += teams) {
-        const float4 a = __ldcg(reinterpret_cast<const float4*>(part + (i * 2 + (i == 0)) * pf) + it);
-        const float w = wt[i * 8 + h];
-        s.x = fmaf(a.x, w, s.x); s.y = fmaf(a.y, w, s.y);
-        s.z = fmaf(a.z, w, s.z); s.w = fmaf(a.w, w, s.w);
-      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+        if (team + u * teams < np) add(ahead[u], team + u * teams);
+#pragma unroll 8
+      for (int i = team + kAhead * teams; i < np; i += teams)
+        add(__ldcg(reinterpret_cast<const float4*>(part + (i * 2 + (i == 0)) * pf) + it), i);
     }
     float4* red = reinterpret_cast<float4*>(sm);
     red[tid] = s;
