@@ -45,6 +45,21 @@ struct Plan {
       off_trace, total;
 };
 
+// theta_i = base^(-2i/d) and their sines: 192 library calls, so the last base's are kept per thread
+struct RopeTables { double base = 0.0, theta[kD / 2], cos1[kD / 2], sin1[kD / 2]; };
+const RopeTables& rope_tables(double base) {
+  static thread_local RopeTables t;
+  if (t.base != base) {
+    for (int i = 0; i < kD / 2; ++i) {
+      t.theta[i] = std::pow(base, -2.0 * i / (double)kD);
+      t.cos1[i] = std::cos(t.theta[i]);
+      t.sin1[i] = std::sin(t.theta[i]);
+    }
+    t.base = base;
+  }
+  return t;
+}
+
 int check_desc(const rtp_layer_desc* d, LayerShape& L) {
   if (!d || !d->slot_of_kv) return RTP_EINVAL;
   if (d->B < 1 || d->B > 4096 || d->Hkv < 1 || d->Hkv > kMaxHkv || d->Hq < 1) return RTP_ESHAPE;
@@ -59,7 +74,7 @@ int check_desc(const rtp_layer_desc* d, LayerShape& L) {
   L.B = d->B; L.Hq = d->Hq; L.Hkv = d->Hkv; L.G = G;
   L.sinks = d->sinks; L.window = d->window; L.ring = d->sinks + d->window;
   L.maxN = d->max_seq_len; L.rope_base = d->rope_base;
-  for (int i = 0; i < kD / 2; ++i) L.theta[i] = std::pow(d->rope_base, -2.0 * i / (double)kD);
+  memcpy(L.theta, rope_tables(d->rope_base).theta, sizeof(L.theta));
   bool seen_r[kMaxHkv] = {false}, seen_l[kMaxHkv] = {false};
   int nr = 0, nl = 0;
   for (int g = 0; g < d->Hkv; ++g) {
@@ -670,13 +685,13 @@ int rtp_paged_reserve(const rtp_page_pool* pool, const int32_t* lens, const int3
   P.cap = std::min<int64_t>((int64_t)pool->table_stride << lg, 0x7fffffffLL);
   P.B = pool->B; P.n_new = n_new; P.n_pages = pool->n_pages; P.stride = pool->table_stride;
   P.lg = lg;
-  P.chunks = std::max({1, (n_new + kResTok - 1) / kResTok,
-                       (pool->table_stride + kResPages - 1) / kResPages});
   P.status = static_cast<int*>(ws);
   P.arrive = at<uint32_t>(ws, 4 * kPagedReserveCounter);
-  // about four items a warp, at most one CTA per SM
-  const int64_t items = (int64_t)P.B * P.chunks;
-  const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(di.sms, items / (4 * kResThreads / 32)));
+  // about two blocks of 32 pages a warp, as far as n_new tells, and at most one CTA per SM: one
+  // CTA for a decode step, which then needs no arrival
+  const int64_t pages = n_new > 0 ? ((int64_t)n_new >> lg) + 2 : pool->table_stride;
+  const int64_t blocks = P.B * ((pages + 31) / 32);
+  const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(di.sms, blocks / (4 * kResWarps)));
   paged_reserve_kernel<<<grid, kResThreads, 8 * (size_t)P.B, (cudaStream_t)stream>>>(P);
   g_launches = 1;
   return cudaGetLastError() == cudaSuccess ? RTP_OK : RTP_ECUDA;
@@ -701,13 +716,23 @@ int rtp_paged_append_kv(const rtp_layer_desc* desc, const rtp_paged_cache* cache
   P.cap_rows = (int64_t)P.C.n_pages << P.C.lg;
   P.Hkv = L.Hkv;
   P.status = static_cast<int*>(ws);
-  memcpy(P.theta, L.theta, sizeof(P.theta));
-  const int64_t grid = (P.n_tok + kPagedAppendTok - 1) / kPagedAppendTok;
+  const RopeTables& rt = rope_tables(desc->rope_base);
+  memcpy(P.theta, rt.theta, sizeof(P.theta));
+  memcpy(P.cos1, rt.cos1, sizeof(P.cos1));
+  memcpy(P.sin1, rt.sin1, sizeof(P.sin1));
+  // 16 tokens a CTA share a quarter of the sines; short calls take one sine per token and angle,
+  // and four times the CTAs
+  const int tok = n_new >= 16 ? 16 : 4;
+  const int64_t grid = (P.n_tok + tok - 1) / tok;
   if (grid > 0x7fffffffLL) return RTP_ESHAPE;
-  if (cache->kv_type == RTP_KV_BF16)
-    paged_append_kernel<kKvBf16><<<(unsigned)grid, 256, 0, (cudaStream_t)stream>>>(P);
-  else
-    paged_append_kernel<kKvE4m3><<<(unsigned)grid, 256, 0, (cudaStream_t)stream>>>(P);
+  cudaStream_t st = (cudaStream_t)stream;
+  if (cache->kv_type == RTP_KV_BF16) {
+    if (tok == 16) paged_append_kernel<kKvBf16, 4><<<(unsigned)grid, 256, 0, st>>>(P);
+    else paged_append_kernel<kKvBf16, 1><<<(unsigned)grid, 256, 0, st>>>(P);
+  } else {
+    if (tok == 16) paged_append_kernel<kKvE4m3, 4><<<(unsigned)grid, 256, 0, st>>>(P);
+    else paged_append_kernel<kKvE4m3, 1><<<(unsigned)grid, 256, 0, st>>>(P);
+  }
   g_launches = 1;
   return cudaGetLastError() == cudaSuccess ? RTP_OK : RTP_ECUDA;
 }

@@ -161,6 +161,21 @@ __device__ __forceinline__ float row_scale(float amax) {
   return fmaxf(__fdiv_rn(amax, kE4m3Max), kScaleMin);
 }
 
+// Four values as e4m3 bytes of x / scale (the quotient in single precision). The quotient is
+// taken by the reciprocal with 2^-21 of doubt, and divided out where that leaves two bytes open.
+__device__ __forceinline__ void e4m3_of4(const float* x, float scale, uint32_t& w) {
+  const float inv = __frcp_rn(scale);
+  float q[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) q[e] = x[e] * inv;
+  const float dn = 1.f - 4.8e-7f, up = 1.f + 4.8e-7f;
+  w = f_e4m3x2(q[0] * dn, q[1] * dn) | f_e4m3x2(q[2] * dn, q[3] * dn) << 16;
+  const uint32_t w1 = f_e4m3x2(q[0] * up, q[1] * up) | f_e4m3x2(q[2] * up, q[3] * up) << 16;
+  if (w != w1 || !(inv < 1e38f))
+    w = f_e4m3x2(__fdiv_rn(x[0], scale), __fdiv_rn(x[1], scale)) |
+        f_e4m3x2(__fdiv_rn(x[2], scale), __fdiv_rn(x[3], scale)) << 16;
+}
+
 // ------------------------------------------------------------------ the line of tiles
 
 // Length of sequence b; 0 (no tiles) for an empty or an invalid one.
@@ -1192,43 +1207,86 @@ struct PagedAppendParams {
   int64_t n_tok, cap_rows;       // B * n_new; n_pages * page
   int n_new, Hkv;
   int* status;
-  double theta[kD / 2];
+  double theta[kD / 2], cos1[kD / 2], sin1[kD / 2];   // theta_i, cos and sin of it
 };
 
-// A CTA takes kPagedAppendTok consecutive tokens of the flattened [B][n_new] axis: their 64
-// angles once for all KV heads (sin and cos in double), then half a warp per (token, KV head)
-// row: 4 channel pairs a lane. Bound by HBM: 512 B read, 512 (264) B written per row.
-constexpr int kPagedAppendTok = 4;
+// Four channels i..i + 3 of a row and their partners 64 on, rotated: bf16 inputs (as floats),
+// (cos, sin) as float pairs high + low; exact products and sums carried as pairs (the error-free
+// transformations of Dekker and Knuth), so each result is the exact one rounded once, up to a
+// relative error of 2^-45.
+__device__ __forceinline__ float rot_sum(float a, float ch, float cl, float b, float sh, float sl) {
+  const float p = a * ch, q = b * sh;                  // a c + b s
+  const float ep = fmaf(a, ch, -p), eq = fmaf(b, sh, -q);
+  const float s = p + q, t = s - p;
+  const float es = (p - (s - t)) + (q - t);
+  return s + (es + (ep + eq + fmaf(a, cl, b * sl)));
+}
 
-template <int KV>
+// A CTA of 256 threads takes 4 R consecutive tokens of the flattened [B][n_new] axis. First the
+// angles, once for all KV heads: sin and cos in double of every R-th token's 64 angles; the R - 1
+// tokens after it, where they belong to the same sequence, by turning one position on. Then half
+// a warp per (token, KV head) row, 4 channel pairs a lane.
+// Bound by HBM: 512 B read, 512 (264) B written per row. What must not take longer: double
+// precision per element does (conversions run at 16 lanes a cycle), so bf16 rows are rotated in
+// single precision with a bound on the error, and only where the bound straddles a border of the
+// bf16 rounding (about 2^-12 of the elements) again in double: the same bits as double throughout.
+// e4m3 rows need the single-precision value itself, and use float pairs.
+template <int KV, int R>
 __global__ void __launch_bounds__(256)
 paged_append_kernel(const __grid_constant__ PagedAppendParams P) {
-  __shared__ double2 ang[kPagedAppendTok][kD / 2];
-  __shared__ int32_t slots[kPagedAppendTok];
+  constexpr int TOK = 4 * R;
+  // bf16: (cos, sin) in double and rounded; e4m3: rounded, then their remainders
+  __shared__ __align__(16) double2 ang[KV == kKvBf16 ? TOK : 1][kD / 2];
+  __shared__ __align__(16) float2 ang2[KV == kKvBf16 ? TOK : 1][kD / 2];
+  __shared__ __align__(16) float4 ang4[KV == kKvBf16 ? 1 : TOK][kD / 2];
+  __shared__ int32_t slots[TOK];
   const int tid = threadIdx.x;
-  const int64_t tok0 = (int64_t)blockIdx.x * kPagedAppendTok;
+  const int64_t tok0 = (int64_t)blockIdx.x * TOK;
   {
-    const int u = tid >> 6, i = tid & 63;
-    const int64_t tok = tok0 + u;
-    int slot = -1;
-    if (tok < P.n_tok) slot = P.slot_map[tok];
-    if (slot >= 0) {
-      const int64_t b = tok / P.n_new;
-      const int64_t pos = (int64_t)P.start_pos[b] + (tok - b * P.n_new);
-      if (slot >= P.cap_rows || pos < 0) {
-        if (i == 0) set_status(P.status, -6);
-        slot = -1;
-      } else {
-        double s, c;
-        rope_sincos((double)pos, P.theta[i], &s, &c);
-        ang[u][i] = make_double2(c, s);
+    const int i = tid & 63;
+    const int64_t first = tok0 + (tid >> 6) * R;
+    const double th = P.theta[i], c1 = P.cos1[i], s1 = P.sin1[i];
+    int64_t b = first < P.n_tok ? first / P.n_new : 0;
+    int64_t j = first - b * P.n_new;
+    double s = 0.0, c = 0.0;
+    bool have = false;
+#pragma unroll
+    for (int r = 0; r < R; ++r, ++j) {
+      if (j == P.n_new) { j = 0; ++b; have = false; }
+      const int64_t tok = first + r;
+      int slot = tok < P.n_tok ? P.slot_map[tok] : -1;
+      if (tok < P.n_tok) {
+        const int64_t pos = (int64_t)P.start_pos[b] + j;
+        if (slot >= 0 && (slot >= P.cap_rows || pos < 0)) {
+          if (i == 0) set_status(P.status, -6);
+          slot = -1;
+        }
+        if (have) {
+          const double c2 = c * c1 - s * s1;
+          s = s * c1 + c * s1;
+          c = c2;
+        } else if (slot >= 0) {
+          rope_sincos((double)pos, th, &s, &c);
+          have = true;
+        }
+        if (slot >= 0) {
+          const int u = (tid >> 6) * R + r;
+          const float cf = (float)c, sf = (float)s;
+          if (KV == kKvBf16) {
+            ang[u][i] = make_double2(c, s);
+            ang2[u][i] = make_float2(cf, sf);
+          } else {
+            ang4[u][i] = make_float4(cf, sf, (float)(c - (double)cf), (float)(s - (double)sf));
+          }
+        }
       }
+      if (i == 0) slots[(tid >> 6) * R + r] = slot;
     }
-    if (i == 0) slots[u] = slot;
   }
   __syncthreads();
   const int half = tid >> 4, ln = tid & 15;
-  for (int it = half; it < kPagedAppendTok * P.Hkv; it += 16) {
+#pragma unroll 2
+  for (int it = half; it < TOK * P.Hkv; it += 16) {
     const int u = it / P.Hkv, g = it - u * P.Hkv;
     const int slot = slots[u];
     if (slot < 0) continue;
@@ -1238,30 +1296,61 @@ paged_append_kernel(const __grid_constant__ PagedAppendParams P) {
     const uint4 vv = __ldg(reinterpret_cast<const uint4*>(P.v + src) + ln);
     const float xa[4] = {bf_lo(a.x), bf_hi(a.x), bf_lo(a.y), bf_hi(a.y)};
     const float xc[4] = {bf_lo(c.x), bf_hi(c.x), bf_lo(c.y), bf_hi(c.y)};
-    double lo[4], hi[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const double2 cs = ang[u][4 * ln + e];
-      lo[e] = (double)xa[e] * cs.x - (double)xc[e] * cs.y;
-      hi[e] = (double)xa[e] * cs.y + (double)xc[e] * cs.x;
-    }
     const int64_t pid = slot >> P.C.lg;
     const int64_t in = ((int64_t)g << P.C.lg) + (slot & ((1 << P.C.lg) - 1));
     const int64_t row = pid * P.C.page_stride + in;
     if (KV == kKvBf16) {
+      uint32_t w[4];                                   // channels i, i+1 | i+2, i+3 | the partners
+      bool unsure = false;
+#pragma unroll
+      for (int e = 0; e < 4; e += 2) {
+        float lo[2][2], hi[2][2];
+#pragma unroll
+        for (int d = 0; d < 2; ++d) {
+          const float2 cs = ang2[u][4 * ln + e + d];
+          const float x = xa[e + d], y = xc[e + d];
+          const float ys = y * cs.y, yc = y * cs.x;
+          const float f = fmaf(x, cs.x, -ys), h = fmaf(x, cs.y, yc);
+          // roundings: of the angles (2^-24 of each product), of one product and of the result:
+          // below 2^-24 (2 |f| + 3 |ys|), and a few of the smallest numbers
+          const float ef = fmaf(fabsf(f) + 2.f * fabsf(ys), 2.4e-7f, 1e-44f);
+          const float eh = fmaf(fabsf(h) + 2.f * fabsf(yc), 2.4e-7f, 1e-44f);
+          unsure = unsure || !(fabsf(f) + fabsf(h) < 3e38f);
+          lo[d][0] = f - ef; lo[d][1] = f + ef;
+          hi[d][0] = h - eh; hi[d][1] = h + eh;
+        }
+        const uint32_t l0 = pack_bf2(lo[0][0], lo[1][0]), l1 = pack_bf2(lo[0][1], lo[1][1]);
+        const uint32_t h0 = pack_bf2(hi[0][0], hi[1][0]), h1 = pack_bf2(hi[0][1], hi[1][1]);
+        w[e >> 1] = l0;
+        w[2 + (e >> 1)] = h0;
+        unsure = unsure || l0 != l1 || h0 != h1;
+      }
+      if (unsure) {
+        double lo[4], hi[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const double2 cs = ang[u][4 * ln + e];
+          lo[e] = (double)xa[e] * cs.x - (double)xc[e] * cs.y;
+          hi[e] = (double)xa[e] * cs.y + (double)xc[e] * cs.x;
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          w[e] = d2bf_rn(lo[2 * e]) | (uint32_t)d2bf_rn(lo[2 * e + 1]) << 16;
+          w[2 + e] = d2bf_rn(hi[2 * e]) | (uint32_t)d2bf_rn(hi[2 * e + 1]) << 16;
+        }
+      }
       unsigned char* kd = P.C.k + row * 256;
-      uint2 w;
-      w.x = d2bf_rn(lo[0]) | (uint32_t)d2bf_rn(lo[1]) << 16;
-      w.y = d2bf_rn(lo[2]) | (uint32_t)d2bf_rn(lo[3]) << 16;
-      reinterpret_cast<uint2*>(kd)[ln] = w;
-      w.x = d2bf_rn(hi[0]) | (uint32_t)d2bf_rn(hi[1]) << 16;
-      w.y = d2bf_rn(hi[2]) | (uint32_t)d2bf_rn(hi[3]) << 16;
-      reinterpret_cast<uint2*>(kd + 128)[ln] = w;
+      reinterpret_cast<uint2*>(kd)[ln] = make_uint2(w[0], w[1]);
+      reinterpret_cast<uint2*>(kd + 128)[ln] = make_uint2(w[2], w[3]);
       reinterpret_cast<uint4*>(P.C.v + row * 256)[ln] = vv;
     } else {
       float k[8], y[8];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) { k[e] = (float)lo[e]; k[4 + e] = (float)hi[e]; }
+      for (int e = 0; e < 4; ++e) {
+        const float4 cs = ang4[u][4 * ln + e];
+        k[e] = rot_sum(xa[e], cs.x, cs.z, -xc[e], cs.y, cs.w);
+        k[4 + e] = rot_sum(xa[e], cs.y, cs.w, xc[e], cs.x, cs.z);
+      }
       unpack8(vv, y);
       float mk = 0.f, mv = 0.f;
 #pragma unroll
@@ -1274,14 +1363,10 @@ paged_append_kernel(const __grid_constant__ PagedAppendParams P) {
       }
       const float sk = row_scale(mk), sv = row_scale(mv);
       uint32_t w[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float* z = e < 2 ? k : y;
-        const float s = e < 2 ? sk : sv;
-        const int j = 4 * (e & 1);
-        w[e] = f_e4m3x2(__fdiv_rn(z[j], s), __fdiv_rn(z[j + 1], s)) |
-               f_e4m3x2(__fdiv_rn(z[j + 2], s), __fdiv_rn(z[j + 3], s)) << 16;
-      }
+      e4m3_of4(k, sk, w[0]);
+      e4m3_of4(k + 4, sk, w[1]);
+      e4m3_of4(y, sv, w[2]);
+      e4m3_of4(y + 4, sv, w[3]);
       unsigned char* kd = P.C.k + row * 128;
       reinterpret_cast<uint32_t*>(kd)[ln] = w[0];
       reinterpret_cast<uint32_t*>(kd + 64)[ln] = w[1];
@@ -1303,137 +1388,158 @@ struct PagedReserveParams {
   const int64_t* counters;
   int64_t* counters_out;
   int64_t cap;                   // tokens a table row can hold
-  int B, n_new, n_pages, stride, lg, chunks;
+  int B, n_new, n_pages, stride, lg;
   int* status;
   uint32_t* arrive;
 };
 
-constexpr int kResThreads = 512;
-constexpr int kResTok = 2048, kResPages = 128;     // tokens and page moves of one warp item
+constexpr int kResThreads = 512, kResWarps = kResThreads / 32;
+constexpr int kResPer = 4096 / kResThreads;        // sequences a thread sums up, at most
 
 // saturating sum of counts (each at most 2^31 - 1)
 __device__ __forceinline__ uint32_t add_sat(uint32_t a, uint32_t b) { return min(a + b, 0x7fffffffu); }
 
-// Exclusive block-wide saturating sums of two counts; totals to tot[2]. scratch: 64 words.
-__device__ __forceinline__ void block_scan2(uint32_t& a, uint32_t& c, uint32_t* scratch,
-                                            uint32_t (&tot)[2]) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint32_t ia = a, ic = c;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t ua = __shfl_up_sync(0xffffffffu, ia, o), uc = __shfl_up_sync(0xffffffffu, ic, o);
-    if (lane >= o) { ia = add_sat(ia, ua); ic = add_sat(ic, uc); }
-  }
-  __syncthreads();
-  if (lane == 31) { scratch[warp] = ia; scratch[32 + warp] = ic; }
-  __syncthreads();
-  uint32_t ba = 0, bc = 0;
-  tot[0] = tot[1] = 0;
-  for (int w = 0; w < kResThreads / 32; ++w) {
-    if (w == warp) { ba = tot[0]; bc = tot[1]; }
-    tot[0] = add_sat(tot[0], scratch[w]);
-    tot[1] = add_sat(tot[1], scratch[32 + w]);
-  }
-  // exclusive: the neighbour's inclusive sum (a saturated one cannot be taken apart)
-  const uint32_t ea = __shfl_up_sync(0xffffffffu, ia, 1), ec = __shfl_up_sync(0xffffffffu, ic, 1);
-  a = add_sat(ba, lane ? ea : 0);
-  c = add_sat(bc, lane ? ec : 0);
+// counter mod n (a 64-bit division only for a counter beyond 2^32)
+__device__ __forceinline__ int ring_place(int64_t x, int n) {
+  return x >> 32 ? (int)(x % n) : (int)((uint32_t)x % (uint32_t)n);
 }
 
-// Every CTA computes the sums over the whole batch (B lengths from L2), then the warps of the
-// grid share out the (sequence, chunk) items: page moves between ring and table, and slots.
+// One sequence's wish: held and wanted pages. Invalid lengths hold and want nothing.
+struct ResWish { int n0, n1, h0, h1; bool bad; };
+__device__ __forceinline__ ResWish res_wish(const PagedReserveParams& P, int b) {
+  ResWish w;
+  w.n0 = P.lens[b];
+  w.n1 = P.new_lens[b];
+  w.bad = w.n0 < 0 || w.n1 < 0 || w.n0 > P.cap || w.n1 > P.cap;
+  const int64_t r = (1 << P.lg) - 1;
+  w.h0 = w.bad ? 0 : (int)((w.n0 + r) >> P.lg);
+  w.h1 = w.bad ? 0 : (int)((w.n1 + r) >> P.lg);
+  return w;
+}
+
+// Every CTA sums up the whole batch (its lengths come from L2): a thread takes up to 8
+// consecutive sequences, one scan over the block. Then the grid's warps share out the sequences,
+// W / B warps to one, 32 pages at a time: a lane per page loads its id (from the ring or the
+// table) once, writes the table entry, and the slots of those pages' tokens take the id by a
+// shuffle. Bound by the slot map's bytes for prompts, by the launch for a decode step.
 // Nothing that a call reads is written before all CTAs have read it: the ring's taken and
 // returned entries are disjoint, held table entries are not rewritten, and the lengths and
 // counters are written by the CTA that arrives last, so they may be updated in place.
 __global__ void __launch_bounds__(kResThreads)
 paged_reserve_kernel(const __grid_constant__ PagedReserveParams P) {
   extern __shared__ uint32_t rsm[];
-  uint32_t* upto = rsm;                      // [B] pages taken before each sequence
+  uint32_t* upto = rsm;                      // [B] pages lacked before each sequence
   uint32_t* back = rsm + P.B;                // [B] pages returned before each sequence
-  __shared__ uint32_t scratch[64];
+  __shared__ uint32_t wsum[2][kResWarps];
   __shared__ uint32_t s_taken, s_bad, s_last;
-  const int tid = threadIdx.x, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) { s_taken = 0; s_bad = 0; }
   const int64_t head = P.counters[0], tail = P.counters[1];
+  const int per = (P.B + kResThreads - 1) / kResThreads, first = tid * per;
+  uint32_t need[kResPer], ret[kResPer], a = 0, c = 0;
+  bool bad = false;
+#pragma unroll
+  for (int k = 0; k < kResPer; ++k) {
+    need[k] = ret[k] = 0;
+    if (k < per && first + k < P.B) {
+      const ResWish w = res_wish(P, first + k);
+      need[k] = max(w.h1 - w.h0, 0);
+      ret[k] = max(w.h0 - w.h1, 0);
+      bad = bad || w.bad;
+    }
+    a = add_sat(a, need[k]);
+    c = add_sat(c, ret[k]);
+  }
+  uint32_t ia = a, ic = c;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t ua = __shfl_up_sync(0xffffffffu, ia, o), uc = __shfl_up_sync(0xffffffffu, ic, o);
+    if (lane >= o) { ia = add_sat(ia, ua); ic = add_sat(ic, uc); }
+  }
+  if (lane == 31) { wsum[0][warp] = ia; wsum[1][warp] = ic; }
+  // exclusive: the neighbour's inclusive sum (a saturated one cannot be taken apart)
+  uint32_t ea = __shfl_up_sync(0xffffffffu, ia, 1), ec = __shfl_up_sync(0xffffffffu, ic, 1);
+  if (lane == 0) ea = ec = 0;
+  __syncthreads();
+  uint32_t run_c;                            // all returned pages
+  {
+    uint32_t va = lane < kResWarps ? wsum[0][lane] : 0, vc = lane < kResWarps ? wsum[1][lane] : 0;
+#pragma unroll
+    for (int o = 1; o < kResWarps; o <<= 1) {
+      const uint32_t ua = __shfl_up_sync(0xffffffffu, va, o), uc = __shfl_up_sync(0xffffffffu, vc, o);
+      if (lane >= o) { va = add_sat(va, ua); vc = add_sat(vc, uc); }
+    }
+    run_c = __shfl_sync(0xffffffffu, vc, kResWarps - 1);
+    const uint32_t ba = __shfl_sync(0xffffffffu, va, max(warp - 1, 0));
+    const uint32_t bc = __shfl_sync(0xffffffffu, vc, max(warp - 1, 0));
+    if (warp > 0) { ea = add_sat(ea, ba); ec = add_sat(ec, bc); }
+  }
   const bool sane = head >= 0 && tail >= head && tail - head <= P.n_pages;
   const uint32_t avail = sane ? (uint32_t)(tail - head) : 0;
-  const int ps1 = (1 << P.lg) - 1;
-  if (tid == 0) { s_taken = 0; s_bad = 0; }
-  __syncthreads();
-  uint32_t run_a = 0, run_c = 0;
-  for (int b0 = 0; b0 < P.B; b0 += kResThreads) {
-    const int b = b0 + tid;
-    uint32_t need = 0, ret = 0;
-    if (b < P.B) {
-      const int n0 = P.lens[b], n1 = P.new_lens[b];
-      if (n0 < 0 || n1 < 0 || n0 > P.cap || n1 > P.cap) {
-        s_bad = 1;
-      } else {
-        const int h0 = (int)(((int64_t)n0 + ps1) >> P.lg), h1 = (int)(((int64_t)n1 + ps1) >> P.lg);
-        if (h1 > h0) need = h1 - h0; else ret = h0 - h1;
-      }
+  uint32_t taken = 0;
+#pragma unroll
+  for (int k = 0; k < kResPer; ++k) {
+    if (k < per && first + k < P.B) {
+      upto[first + k] = ea;
+      back[first + k] = ec;
     }
-    uint32_t a = need, c = ret, tot[2];
-    block_scan2(a, c, scratch, tot);
-    a = add_sat(run_a, a);
-    c = add_sat(run_c, c);
-    if (b < P.B) {
-      upto[b] = a;
-      back[b] = c;
-      const uint32_t end = add_sat(a, need);
-      if (need && end <= avail) atomicMax(&s_taken, end);
-    }
-    run_a = add_sat(run_a, tot[0]);
-    run_c = add_sat(run_c, tot[1]);
+    ea = add_sat(ea, need[k]);
+    ec = add_sat(ec, ret[k]);
+    if (need[k] && ea <= avail) taken = ea;
   }
+  taken = __reduce_max_sync(0xffffffffu, taken);
+  if (lane == 0 && taken) atomicMax(&s_taken, taken);
+  if (bad) s_bad = 1;
   __syncthreads();
   // more pages than the ring has room for: the lengths or counters are not this pool's
   const bool ok = sane && (int64_t)avail + run_c <= P.n_pages;
   if (tid == 0 && blockIdx.x == 0 && (!ok || s_bad)) set_status(P.status, -6);
-  const int hm = ok ? (int)(head % P.n_pages) : 0, tm = ok ? (int)(tail % P.n_pages) : 0;
-  const int warps = gridDim.x * (kResThreads / 32);
-  const int64_t items = (int64_t)P.B * P.chunks;
-  for (int64_t it = (int64_t)blockIdx.x * (kResThreads / 32) + (tid >> 5); it < items; it += warps) {
-    const int b = (int)(it / P.chunks), ch = (int)(it - (int64_t)b * P.chunks);
-    int n0 = P.lens[b], n1 = P.new_lens[b];
-    if (n0 < 0 || n1 < 0 || n0 > P.cap || n1 > P.cap) n1 = n0 = 0;     // no slots, no moves
-    const int h0 = (int)(((int64_t)n0 + ps1) >> P.lg), h1 = (int)(((int64_t)n1 + ps1) >> P.lg);
+  const int hm = ok ? ring_place(head, P.n_pages) : 0, tm = ok ? ring_place(tail, P.n_pages) : 0;
+
+  const int W = gridDim.x * kResWarps, share = max(1, W / P.B);     // warps of a sequence
+  const int w = blockIdx.x * kResWarps + warp, teams = W / share;
+  for (int b = w / share; b < P.B && w < teams * share; b += teams) {
+    const ResWish x = res_wish(P, b);
     const int64_t u0 = upto[b], r0 = back[b];
-    const bool granted = ok && (h1 <= h0 || u0 + (h1 - h0) <= avail);
-    if (!granted) n1 = n0;
+    const bool granted = ok && !x.bad && (x.h1 <= x.h0 || u0 + (x.h1 - x.h0) <= avail);
+    const int n1 = granted ? x.n1 : x.n0, h1 = granted ? x.h1 : x.h0;
     int32_t* row = P.table + (int64_t)b * P.stride;
-    if (granted) {
-      const int m1 = min(abs(h1 - h0), (ch + 1) * kResPages);
-      for (int j = ch * kResPages + lane; j < m1; j += 32) {
-        if (h1 > h0) {
-          int64_t at = hm + u0 + j;
-          if (at >= P.n_pages) at -= P.n_pages;
-          row[h0 + j] = P.free_pages[at];
-        } else {
-          int64_t at = tm + r0 + j;
-          if (at >= P.n_pages) at -= P.n_pages;
-          P.free_pages[at] = row[h1 + j];
-        }
-      }
-    }
-    const int t1 = min(P.n_new, (ch + 1) * kResTok);
     int32_t* slots = P.slot_map + (int64_t)b * P.n_new;
-    for (int j = ch * kResTok + lane; j < t1; j += 32) {
-      const int64_t pos = (int64_t)n0 + j;
-      int slot = -1;
-      if (pos < n1) {
-        const int pg = (int)(pos >> P.lg);
-        int id;
-        if (pg < h0) {
-          id = row[pg];
-        } else {
-          int64_t at = hm + u0 + (pg - h0);
-          if (at >= P.n_pages) at -= P.n_pages;
-          id = P.free_pages[at];
-        }
-        slot = (id << P.lg) + (int)(pos & ps1);
-      }
-      slots[j] = slot;
+    // pages returned
+    for (int j = (w % share) * 32 + lane; j < x.h0 - h1; j += 32 * share) {
+      int64_t at = tm + r0 + j;
+      if (at >= P.n_pages) at -= P.n_pages;
+      P.free_pages[at] = row[h1 + j];
     }
+    // pages from the one that the first new token goes to, 32 at a time; then the places of
+    // slot_map behind the last page
+    const int pg0 = x.bad ? 0 : x.n0 >> P.lg;
+    const int chunks = max(h1 - pg0, 0) + 31 >> 5;
+    for (int ch = w % share; ch < chunks; ch += share) {
+      const int pg = pg0 + 32 * ch + lane;
+      int id = 0;
+      if (pg < x.h0) {
+        id = row[pg];
+      } else if (pg < h1) {
+        int64_t at = hm + u0 + (pg - x.h0);
+        if (at >= P.n_pages) at -= P.n_pages;
+        id = P.free_pages[at];
+        row[pg] = id;
+      }
+      // tokens of these pages: positions from p0, at least n0
+      const int64_t p0 = (int64_t)(pg0 + 32 * ch) << P.lg;
+      const int64_t end = min(min(p0 + (32 << P.lg), (int64_t)n1), (int64_t)x.n0 + P.n_new);
+      const int64_t start = max(p0, (int64_t)x.n0);
+#pragma unroll 4
+      for (int64_t p = start; p < end; p += 32) {
+        const int64_t pos = p + lane;
+        const int pid = __shfl_sync(0xffffffffu, id, (int)(min(pos, end - 1) - p0) >> P.lg);
+        if (pos < end) slots[pos - x.n0] = (pid << P.lg) + (int)(pos & ((1 << P.lg) - 1));
+      }
+    }
+    const int got = min(max(n1 - x.n0, 0), P.n_new);
+    for (int j = (x.bad ? 0 : got) + (w % share) * 32 + lane; j < P.n_new; j += 32 * share)
+      slots[j] = -1;
   }
   // lengths and counters, once every CTA has read them
   __syncthreads();
@@ -1441,13 +1547,9 @@ paged_reserve_kernel(const __grid_constant__ PagedReserveParams P) {
   __syncthreads();
   if (!s_last) return;
   for (int b = tid; b < P.B; b += kResThreads) {
-    const int n0 = P.lens[b], n1 = P.new_lens[b];
-    int n = n0;
-    if (ok && !(n0 < 0 || n1 < 0 || n0 > P.cap || n1 > P.cap)) {
-      const int h0 = (int)(((int64_t)n0 + ps1) >> P.lg), h1 = (int)(((int64_t)n1 + ps1) >> P.lg);
-      if (h1 <= h0 || (int64_t)upto[b] + (h1 - h0) <= avail) n = n1;
-    }
-    P.lens_out[b] = n;
+    const ResWish x = res_wish(P, b);
+    const bool granted = ok && !x.bad && (x.h1 <= x.h0 || (int64_t)upto[b] + (x.h1 - x.h0) <= avail);
+    P.lens_out[b] = granted ? x.n1 : x.n0;
   }
   if (tid == 0) {
     P.counters_out[0] = ok ? head + s_taken : head;
