@@ -715,23 +715,31 @@ int rtp_paged_append_kv(const rtp_layer_desc* desc, const rtp_paged_cache* cache
   P.n_new = n_new; P.n_tok = (int64_t)L.B * n_new;
   P.cap_rows = (int64_t)P.C.n_pages << P.C.lg;
   P.Hkv = L.Hkv;
+  const int heads = std::min(L.Hkv, kAppendHeads), groups = (L.Hkv + kAppendHeads - 1) / kAppendHeads;
+  const int last = L.Hkv - (groups - 1) * kAppendHeads;
+  P.inv_last = (65536u + last - 1) / last;
+  P.step_last = 8 / last;
   P.status = static_cast<int*>(ws);
   const RopeTables& rt = rope_tables(desc->rope_base);
   memcpy(P.theta, rt.theta, sizeof(P.theta));
   memcpy(P.cos1, rt.cos1, sizeof(P.cos1));
   memcpy(P.sin1, rt.sin1, sizeof(P.sin1));
-  // 16 tokens a CTA share a quarter of the sines; short calls take one sine per token and angle,
-  // and four times the CTAs
-  const int tok = n_new >= 16 ? 16 : 4;
-  const int64_t grid = (P.n_tok + tok - 1) / tok;
-  if (grid > 0x7fffffffLL) return RTP_ESHAPE;
+  // short calls take a sine per token and angle, and more CTAs; long ones share it among
+  // neighbouring tokens, the more the fewer rows a token has
+  const int r = n_new < 16 ? 1 : heads <= 2 ? 4 : 2;
+  const int64_t gx = (P.n_tok + 4 * r - 1) / (4 * r);
+  if (gx > 0x7fffffffLL) return RTP_ESHAPE;
+  const dim3 grid((unsigned)gx, groups);
+  const int smem = 4 * r * (1024 + heads * 512);       // at most 40 KB
   cudaStream_t st = (cudaStream_t)stream;
   if (cache->kv_type == RTP_KV_BF16) {
-    if (tok == 16) paged_append_kernel<kKvBf16, 4><<<(unsigned)grid, 256, 0, st>>>(P);
-    else paged_append_kernel<kKvBf16, 1><<<(unsigned)grid, 256, 0, st>>>(P);
+    if (r == 1) paged_append_kernel<kKvBf16, 1><<<grid, 256, smem, st>>>(P);
+    else if (r == 2) paged_append_kernel<kKvBf16, 2><<<grid, 256, smem, st>>>(P);
+    else paged_append_kernel<kKvBf16, 4><<<grid, 256, smem, st>>>(P);
   } else {
-    if (tok == 16) paged_append_kernel<kKvE4m3, 4><<<(unsigned)grid, 256, 0, st>>>(P);
-    else paged_append_kernel<kKvE4m3, 1><<<(unsigned)grid, 256, 0, st>>>(P);
+    if (r == 1) paged_append_kernel<kKvE4m3, 1><<<grid, 256, smem, st>>>(P);
+    else if (r == 2) paged_append_kernel<kKvE4m3, 2><<<grid, 256, smem, st>>>(P);
+    else paged_append_kernel<kKvE4m3, 4><<<grid, 256, smem, st>>>(P);
   }
   g_launches = 1;
   return cudaGetLastError() == cudaSuccess ? RTP_OK : RTP_ECUDA;

@@ -161,19 +161,20 @@ __device__ __forceinline__ float row_scale(float amax) {
   return fmaxf(__fdiv_rn(amax, kE4m3Max), kScaleMin);
 }
 
-// Four values as e4m3 bytes of x / scale (the quotient in single precision). The quotient is
-// taken by the reciprocal with 2^-21 of doubt, and divided out where that leaves two bytes open.
-__device__ __forceinline__ void e4m3_of4(const float* x, float scale, uint32_t& w) {
-  const float inv = __frcp_rn(scale);
+// Four values as e4m3 bytes of x / scale, inv = 1 / scale rounded. The quotient in single
+// precision, rounded once: an estimate and Markstein's correction by its exact remainder. Where
+// the remainder could be too small a number for that, the values are divided.
+__device__ __forceinline__ uint32_t e4m3_of4(const float* x, float scale, float inv) {
   float q[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) q[e] = x[e] * inv;
-  const float dn = 1.f - 4.8e-7f, up = 1.f + 4.8e-7f;
-  w = f_e4m3x2(q[0] * dn, q[1] * dn) | f_e4m3x2(q[2] * dn, q[3] * dn) << 16;
-  const uint32_t w1 = f_e4m3x2(q[0] * up, q[1] * up) | f_e4m3x2(q[2] * up, q[3] * up) << 16;
-  if (w != w1 || !(inv < 1e38f))
-    w = f_e4m3x2(__fdiv_rn(x[0], scale), __fdiv_rn(x[1], scale)) |
-        f_e4m3x2(__fdiv_rn(x[2], scale), __fdiv_rn(x[3], scale)) << 16;
+  for (int e = 0; e < 4; ++e) {
+    q[e] = x[e] * inv;
+    q[e] = fmaf(fmaf(-q[e], scale, x[e]), inv, q[e]);
+  }
+  if (scale < 1e-25f || !(scale < 1e38f))
+#pragma unroll
+    for (int e = 0; e < 4; ++e) q[e] = __fdiv_rn(x[e], scale);
+  return f_e4m3x2(q[0], q[1]) | f_e4m3x2(q[2], q[3]) << 16;
 }
 
 // ------------------------------------------------------------------ the line of tiles
@@ -1206,151 +1207,154 @@ struct PagedAppendParams {
   const int32_t *start_pos, *slot_map;
   int64_t n_tok, cap_rows;       // B * n_new; n_pages * page
   int n_new, Hkv;
+  uint32_t inv_last;             // 2^16 / (heads of the last block of 8) rounded up: divides exactly
+  int step_last;                 // tokens that 256 threads copy at once in the last block
   int* status;
   double theta[kD / 2], cos1[kD / 2], sin1[kD / 2];   // theta_i, cos and sin of it
 };
 
-// Four channels i..i + 3 of a row and their partners 64 on, rotated: bf16 inputs (as floats),
-// (cos, sin) as float pairs high + low; exact products and sums carried as pairs (the error-free
-// transformations of Dekker and Knuth), so each result is the exact one rounded once, up to a
-// relative error of 2^-45.
-__device__ __forceinline__ float rot_sum(float a, float ch, float cl, float b, float sh, float sl) {
-  const float p = a * ch, q = b * sh;                  // a c + b s
-  const float ep = fmaf(a, ch, -p), eq = fmaf(b, sh, -q);
-  const float s = p + q, t = s - p;
-  const float es = (p - (s - t)) + (q - t);
-  return s + (es + (ep + eq + fmaf(a, cl, b * sl)));
-}
+// A CTA of 256 threads takes up to 8 KV heads of 4 R consecutive tokens of the flattened
+// [B][n_new] axis. Their rows, contiguous in the inputs, are copied to shared memory while the
+// angles are made, once for all heads: sin and cos in double of the first token's 64 angles, the
+// other tokens of its sequence by turning on (products of cos and sin of theta). Then half a warp
+// per (token, KV head) row, 4 channel pairs a lane, in double.
+// Bound by HBM: 512 B read, 512 (264) B written per row; what competes is instruction issue
+// (about 110 a row pair) and the conversions to and from double, 16 lanes a cycle. Single
+// precision with carried errors took twice the instructions.
+constexpr int kAppendHeads = 8;
 
-// A CTA of 256 threads takes 4 R consecutive tokens of the flattened [B][n_new] axis. First the
-// angles, once for all KV heads: sin and cos in double of every R-th token's 64 angles; the R - 1
-// tokens after it, where they belong to the same sequence, by turning one position on. Then half
-// a warp per (token, KV head) row, 4 channel pairs a lane.
-// Bound by HBM: 512 B read, 512 (264) B written per row. What must not take longer: double
-// precision per element does (conversions run at 16 lanes a cycle), so bf16 rows are rotated in
-// single precision with a bound on the error, and only where the bound straddles a border of the
-// bf16 rounding (about 2^-12 of the elements) again in double: the same bits as double throughout.
-// e4m3 rows need the single-precision value itself, and use float pairs.
 template <int KV, int R>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 4)
 paged_append_kernel(const __grid_constant__ PagedAppendParams P) {
   constexpr int TOK = 4 * R;
-  // bf16: (cos, sin) in double and rounded; e4m3: rounded, then their remainders
-  __shared__ __align__(16) double2 ang[KV == kKvBf16 ? TOK : 1][kD / 2];
-  __shared__ __align__(16) float2 ang2[KV == kKvBf16 ? TOK : 1][kD / 2];
-  __shared__ __align__(16) float4 ang4[KV == kKvBf16 ? 1 : TOK][kD / 2];
+  // (cos, sin) as the lanes read them: [token][channel % 4][channel / 4]; the tokens' K and V rows
+  extern __shared__ __align__(16) unsigned char asm_[];
+  double2(*ang)[4][16] = reinterpret_cast<double2(*)[4][16]>(asm_);
+  unsigned char* rows = asm_ + TOK * 1024;
   __shared__ int32_t slots[TOK];
   const int tid = threadIdx.x;
   const int64_t tok0 = (int64_t)blockIdx.x * TOK;
+  const int g0 = blockIdx.y * kAppendHeads, heads = min(P.Hkv - g0, kAppendHeads);
+  const bool last_y = blockIdx.y == gridDim.y - 1;
   {
-    const int i = tid & 63;
-    const int64_t first = tok0 + (tid >> 6) * R;
+    // a token's K and V are 32 * heads pieces of 16 bytes; a pass covers as many whole tokens as
+    // there are threads for
+    const int per = heads * 32, u0 = (int)((uint32_t)(tid >> 5) * (last_y ? P.inv_last : 8192u) >> 16);
+    const int x = tid - u0 * per, step = last_y ? P.step_last : 1;
+    const bool isk = x < heads * 16;
+    const uint16_t* src = (isk ? P.k_pre : P.v) + ((tok0 + u0) * P.Hkv + g0) * kD +
+                          (isk ? x : x - heads * 16) * 8;
+    if (u0 < step) {
+      uint32_t dst = smem_u32(rows) + tid * 16;
+#pragma unroll 4
+      for (int u = u0; u < TOK; u += step, src += (int64_t)step * P.Hkv * kD, dst += step * per * 16)
+        if (tok0 + u < P.n_tok && P.slot_map[tok0 + u] >= 0) cp_async16_s(dst, src);
+    }
+    cp_async_commit();
+  }
+  {
+    const int i = tid & 63, sub = tid >> 6;
     const double th = P.theta[i], c1 = P.cos1[i], s1 = P.sin1[i];
-    int64_t b = first < P.n_tok ? first / P.n_new : 0;
-    int64_t j = first - b * P.n_new;
-    double s = 0.0, c = 0.0;
-    bool have = false;
+    const int64_t b0 = P.n_tok >> 32 ? tok0 / P.n_new : (uint32_t)tok0 / (uint32_t)P.n_new;
+    const int64_t j0 = tok0 - b0 * P.n_new;
+    int64_t b = b0, j = j0 + sub * R;
+    bool turn = sub > 0 && j < P.n_new;                // the first token's sequence: turned on
+    while (j >= P.n_new) { j -= P.n_new; ++b; }
+    double s = 0.0, c = 1.0;
+    if (tok0 + sub * R < P.n_tok && !turn) rope_sincos((double)P.start_pos[b] + (double)j, th, &s, &c);
+    if (sub == 0) ang[0][i & 3][i >> 2] = make_double2(c, s);
+    __syncthreads();
+    if (turn) {
+      const double2 z = ang[0][i & 3][i >> 2];
+      c = z.x;
+      s = z.y;
+      double pc = c1, ps = s1;
 #pragma unroll
-    for (int r = 0; r < R; ++r, ++j) {
-      if (j == P.n_new) { j = 0; ++b; have = false; }
-      const int64_t tok = first + r;
-      int slot = tok < P.n_tok ? P.slot_map[tok] : -1;
-      if (tok < P.n_tok) {
-        const int64_t pos = (int64_t)P.start_pos[b] + j;
-        if (slot >= 0 && (slot >= P.cap_rows || pos < 0)) {
+      for (int bit = 1; bit < TOK; bit <<= 1) {
+        if ((sub * R) & bit) {
+          const double t = c * pc - s * ps;
+          s = s * pc + c * ps;
+          c = t;
+        }
+        const double t = pc * pc - ps * ps;
+        ps = 2.0 * pc * ps;
+        pc = t;
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int u = sub * R + r;
+      int slot = -1;
+      if (tok0 + u < P.n_tok) {
+        if (r > 0) {
+          if (++j == P.n_new) {                        // the next sequence begins
+            j = 0;
+            ++b;
+            rope_sincos((double)P.start_pos[b], th, &s, &c);
+          } else {
+            const double t = c * c1 - s * s1;
+            s = s * c1 + c * s1;
+            c = t;
+          }
+        }
+        slot = P.slot_map[tok0 + u];
+        if (slot >= 0 && (slot >= P.cap_rows || (int64_t)P.start_pos[b] + j < 0)) {
           if (i == 0) set_status(P.status, -6);
           slot = -1;
         }
-        if (have) {
-          const double c2 = c * c1 - s * s1;
-          s = s * c1 + c * s1;
-          c = c2;
-        } else if (slot >= 0) {
-          rope_sincos((double)pos, th, &s, &c);
-          have = true;
-        }
-        if (slot >= 0) {
-          const int u = (tid >> 6) * R + r;
-          const float cf = (float)c, sf = (float)s;
-          if (KV == kKvBf16) {
-            ang[u][i] = make_double2(c, s);
-            ang2[u][i] = make_float2(cf, sf);
-          } else {
-            ang4[u][i] = make_float4(cf, sf, (float)(c - (double)cf), (float)(s - (double)sf));
-          }
-        }
+        if (u > 0) ang[u][i & 3][i >> 2] = make_double2(c, s);
       }
-      if (i == 0) slots[(tid >> 6) * R + r] = slot;
+      if (i == 0) slots[u] = slot;
     }
   }
+  cp_async_wait<0>();
   __syncthreads();
-  const int half = tid >> 4, ln = tid & 15;
-#pragma unroll 2
-  for (int it = half; it < TOK * P.Hkv; it += 16) {
-    const int u = it / P.Hkv, g = it - u * P.Hkv;
-    const int slot = slots[u];
+  const int ln = tid & 15;
+  for (int it = tid >> 4; it < TOK * heads; it += 16) {
+    const int u = (int)((uint32_t)it * (last_y ? P.inv_last : 8192u) >> 16);
+    const int g = it - u * heads, slot = slots[u];
     if (slot < 0) continue;
-    const int64_t src = ((tok0 + u) * P.Hkv + g) * kD;
-    const uint2 a = __ldg(reinterpret_cast<const uint2*>(P.k_pre + src) + ln);
-    const uint2 c = __ldg(reinterpret_cast<const uint2*>(P.k_pre + src + 64) + ln);
-    const uint4 vv = __ldg(reinterpret_cast<const uint4*>(P.v + src) + ln);
-    const float xa[4] = {bf_lo(a.x), bf_hi(a.x), bf_lo(a.y), bf_hi(a.y)};
-    const float xc[4] = {bf_lo(c.x), bf_hi(c.x), bf_lo(c.y), bf_hi(c.y)};
-    const int64_t pid = slot >> P.C.lg;
-    const int64_t in = ((int64_t)g << P.C.lg) + (slot & ((1 << P.C.lg) - 1));
+    const unsigned char* kr = rows + (u * heads * 2 + g) * 256;
+    const uint2 a = reinterpret_cast<const uint2*>(kr)[ln];
+    const uint2 c = reinterpret_cast<const uint2*>(kr + 128)[ln];
+    const uint4 vv = reinterpret_cast<const uint4*>(kr + heads * 256)[ln];
+    double kx[8];                                      // channels 4 ln .. 4 ln + 3, their partners
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t wa = e & 2 ? a.y : a.x, wc = e & 2 ? c.y : c.x;
+      const double p = e & 1 ? bf_hi(wa) : bf_lo(wa), q = e & 1 ? bf_hi(wc) : bf_lo(wc);
+      const double2 z = ang[u][e][ln];
+      kx[e] = p * z.x - q * z.y;
+      kx[4 + e] = p * z.y + q * z.x;
+    }
+    float k[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) k[e] = (float)kx[e];
+    const int pid = slot >> P.C.lg;
+    const int in = ((g0 + g) << P.C.lg) + (slot & ((1 << P.C.lg) - 1));
     const int64_t row = pid * P.C.page_stride + in;
     if (KV == kKvBf16) {
-      uint32_t w[4];                                   // channels i, i+1 | i+2, i+3 | the partners
+      // rounding twice differs from once only where single precision ends up in the middle of two
+      // bf16 values (2^-16 of the elements), or has lost a small number's last places
+      uint32_t o[4];
       bool unsure = false;
 #pragma unroll
-      for (int e = 0; e < 4; e += 2) {
-        float lo[2][2], hi[2][2];
-#pragma unroll
-        for (int d = 0; d < 2; ++d) {
-          const float2 cs = ang2[u][4 * ln + e + d];
-          const float x = xa[e + d], y = xc[e + d];
-          const float ys = y * cs.y, yc = y * cs.x;
-          const float f = fmaf(x, cs.x, -ys), h = fmaf(x, cs.y, yc);
-          // roundings: of the angles (2^-24 of each product), of one product and of the result:
-          // below 2^-24 (2 |f| + 3 |ys|), and a few of the smallest numbers
-          const float ef = fmaf(fabsf(f) + 2.f * fabsf(ys), 2.4e-7f, 1e-44f);
-          const float eh = fmaf(fabsf(h) + 2.f * fabsf(yc), 2.4e-7f, 1e-44f);
-          unsure = unsure || !(fabsf(f) + fabsf(h) < 3e38f);
-          lo[d][0] = f - ef; lo[d][1] = f + ef;
-          hi[d][0] = h - eh; hi[d][1] = h + eh;
-        }
-        const uint32_t l0 = pack_bf2(lo[0][0], lo[1][0]), l1 = pack_bf2(lo[0][1], lo[1][1]);
-        const uint32_t h0 = pack_bf2(hi[0][0], hi[1][0]), h1 = pack_bf2(hi[0][1], hi[1][1]);
-        w[e >> 1] = l0;
-        w[2 + (e >> 1)] = h0;
-        unsure = unsure || l0 != l1 || h0 != h1;
+      for (int e = 0; e < 4; ++e) {
+        o[e] = pack_bf2(k[2 * e], k[2 * e + 1]);
+        unsure = unsure || (__float_as_uint(k[2 * e]) & 0xffffu) == 0x8000u ||
+                 (__float_as_uint(k[2 * e + 1]) & 0xffffu) == 0x8000u;
       }
       if (unsure) {
-        double lo[4], hi[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const double2 cs = ang[u][4 * ln + e];
-          lo[e] = (double)xa[e] * cs.x - (double)xc[e] * cs.y;
-          hi[e] = (double)xa[e] * cs.y + (double)xc[e] * cs.x;
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          w[e] = d2bf_rn(lo[2 * e]) | (uint32_t)d2bf_rn(lo[2 * e + 1]) << 16;
-          w[2 + e] = d2bf_rn(hi[2 * e]) | (uint32_t)d2bf_rn(hi[2 * e + 1]) << 16;
-        }
+        for (int e = 0; e < 4; ++e)
+          o[e] = d2bf_rn(kx[2 * e]) | (uint32_t)d2bf_rn(kx[2 * e + 1]) << 16;
       }
       unsigned char* kd = P.C.k + row * 256;
-      reinterpret_cast<uint2*>(kd)[ln] = make_uint2(w[0], w[1]);
-      reinterpret_cast<uint2*>(kd + 128)[ln] = make_uint2(w[2], w[3]);
+      reinterpret_cast<uint2*>(kd)[ln] = make_uint2(o[0], o[1]);
+      reinterpret_cast<uint2*>(kd + 128)[ln] = make_uint2(o[2], o[3]);
       reinterpret_cast<uint4*>(P.C.v + row * 256)[ln] = vv;
     } else {
-      float k[8], y[8];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float4 cs = ang4[u][4 * ln + e];
-        k[e] = rot_sum(xa[e], cs.x, cs.z, -xc[e], cs.y, cs.w);
-        k[4 + e] = rot_sum(xa[e], cs.y, cs.w, xc[e], cs.x, cs.z);
-      }
+      float y[8];
       unpack8(vv, y);
       float mk = 0.f, mv = 0.f;
 #pragma unroll
@@ -1361,21 +1365,17 @@ paged_append_kernel(const __grid_constant__ PagedAppendParams P) {
         mk = fmaxf(mk, __shfl_xor_sync(team, mk, o));
         mv = fmaxf(mv, __shfl_xor_sync(team, mv, o));
       }
-      const float sk = row_scale(mk), sv = row_scale(mv);
-      uint32_t w[4];
-      e4m3_of4(k, sk, w[0]);
-      e4m3_of4(k + 4, sk, w[1]);
-      e4m3_of4(y, sv, w[2]);
-      e4m3_of4(y + 4, sv, w[3]);
+      // one division for both scales: even lanes the keys', odd lanes the values'
+      const float sc = row_scale(ln & 1 ? mv : mk), inv = __frcp_rn(sc);
+      const float sc2 = __shfl_xor_sync(team, sc, 1), inv2 = __shfl_xor_sync(team, inv, 1);
+      const float sk = ln & 1 ? sc2 : sc, ik = ln & 1 ? inv2 : inv;
+      const float sv = ln & 1 ? sc : sc2, iv = ln & 1 ? inv : inv2;
       unsigned char* kd = P.C.k + row * 128;
-      reinterpret_cast<uint32_t*>(kd)[ln] = w[0];
-      reinterpret_cast<uint32_t*>(kd + 64)[ln] = w[1];
-      reinterpret_cast<uint2*>(P.C.v + row * 128)[ln] = make_uint2(w[2], w[3]);
-      if (ln == 0) {
-        const int64_t srow = pid * ((int64_t)P.Hkv << P.C.lg) + in;
-        P.C.ks[srow] = sk;
-        P.C.vs[srow] = sv;
-      }
+      reinterpret_cast<uint32_t*>(kd)[ln] = e4m3_of4(k, sk, ik);
+      reinterpret_cast<uint32_t*>(kd + 64)[ln] = e4m3_of4(k + 4, sk, ik);
+      reinterpret_cast<uint2*>(P.C.v + row * 128)[ln] =
+          make_uint2(e4m3_of4(y, sv, iv), e4m3_of4(y + 4, sv, iv));
+      if (ln < 2) (ln ? P.C.vs : P.C.ks)[pid * ((int64_t)P.Hkv << P.C.lg) + in] = sc;
     }
   }
 }
