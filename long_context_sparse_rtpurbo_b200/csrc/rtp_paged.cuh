@@ -1236,6 +1236,10 @@ paged_append_kernel(const __grid_constant__ PagedAppendParams P) {
   const int64_t tok0 = (int64_t)blockIdx.x * TOK;
   const int g0 = blockIdx.y * kAppendHeads, heads = min(P.Hkv - g0, kAppendHeads);
   const bool last_y = blockIdx.y == gridDim.y - 1;
+  int slot = -1;
+  if (tid < TOK && tok0 + tid < P.n_tok) slot = P.slot_map[tok0 + tid];
+  if (tid < TOK) slots[tid] = slot;
+  if (!__syncthreads_or(slot >= 0)) return;            // a CTA of padding
   {
     // a token's K and V are 32 * heads pieces of 16 bytes; a pass covers as many whole tokens as
     // there are threads for
@@ -1248,7 +1252,7 @@ paged_append_kernel(const __grid_constant__ PagedAppendParams P) {
       uint32_t dst = smem_u32(rows) + tid * 16;
 #pragma unroll 4
       for (int u = u0; u < TOK; u += step, src += (int64_t)step * P.Hkv * kD, dst += step * per * 16)
-        if (tok0 + u < P.n_tok && P.slot_map[tok0 + u] >= 0) cp_async16_s(dst, src);
+        if (slots[u] >= 0) cp_async16_s(dst, src);
     }
     cp_async_commit();
   }
@@ -1284,7 +1288,6 @@ paged_append_kernel(const __grid_constant__ PagedAppendParams P) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const int u = sub * R + r;
-      int slot = -1;
       if (tok0 + u < P.n_tok) {
         if (r > 0) {
           if (++j == P.n_new) {                        // the next sequence begins
@@ -1297,14 +1300,12 @@ paged_append_kernel(const __grid_constant__ PagedAppendParams P) {
             c = t;
           }
         }
-        slot = P.slot_map[tok0 + u];
-        if (slot >= 0 && (slot >= P.cap_rows || (int64_t)P.start_pos[b] + j < 0)) {
-          if (i == 0) set_status(P.status, -6);
-          slot = -1;
+        if (i == 0 && slots[u] >= 0 && (slots[u] >= P.cap_rows || (int64_t)P.start_pos[b] + j < 0)) {
+          set_status(P.status, -6);
+          slots[u] = -1;
         }
         if (u > 0) ang[u][i & 3][i >> 2] = make_double2(c, s);
       }
-      if (i == 0) slots[u] = slot;
     }
   }
   cp_async_wait<0>();
