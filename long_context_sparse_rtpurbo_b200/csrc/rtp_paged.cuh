@@ -212,12 +212,17 @@ __device__ __forceinline__ long long seq_places(const LayerShape& L, int n) {
 struct Cursor {
   int b, gi, k, nt, n, lens;
   int ns, sh, lo;                // tile k covers rows from 16 (k < ns ? k : k + sh); window from lo
+  int kvrow;                     // first row of the KV head in a page
+  const int32_t* pages;          // the sequence's page ids
 };
 
 __device__ __forceinline__ int kv_head(const LayerShape& L, int gi) {
   return gi < L.n_ret ? L.ret_kv[gi] : L.loc_kv[gi - L.n_ret];
 }
-__device__ __forceinline__ void cursor_group(const LayerShape& L, Cursor& c) {
+__device__ __forceinline__ void cursor_group(const PagedDecodeParams& P, Cursor& c) {
+  const LayerShape& L = P.L;
+  c.kvrow = kv_head(L, min(c.gi, L.Hkv - 1)) << P.C.lg;
+  c.pages = P.C.table + (int64_t)c.b * P.C.table_stride;
   if (c.gi < L.n_ret) {
     c.ns = 0; c.sh = 0; c.lo = 0; c.nt = (c.n + 15) >> 4;
   } else {
@@ -235,7 +240,7 @@ __device__ __forceinline__ void cursor_next_group(const PagedDecodeParams& P, Cu
       c.n = __shfl_sync(0xffffffffu, c.lens, c.b & 31);
     } while (c.n == 0 && c.b < P.L.B);
   }
-  cursor_group(P.L, c);
+  cursor_group(P, c);
 }
 // The cursor of the first tile at or after a place of the line, rel places after the start of a
 // chunk of 32 sequences. lens: this lane's length of the chunk; incl and mine: its places with
@@ -269,7 +274,7 @@ __device__ __forceinline__ Cursor cursor_at(const PagedDecodeParams& P, int chun
   *before = place - groups * kSetup - min(k, kSetup);
   *first = place + max(kSetup - k, 0);
   c.k = max(k - kSetup, 0);
-  cursor_group(P.L, c);
+  cursor_group(P, c);
   return c;
 }
 __device__ __forceinline__ long long warp_incl_sum(long long x) {
@@ -317,9 +322,11 @@ struct TileDesc { int pid, row; uint32_t mask; };   // page, row in the page blo
 __device__ __forceinline__ TileDesc tile_desc(const PagedDecodeParams& P, const Cursor& c) {
   const int pos = 16 * (c.k < c.ns ? c.k : c.k + c.sh);
   TileDesc d;
-  d.pid = __ldg(P.C.table + (int64_t)c.b * P.C.table_stride + (pos >> P.C.lg));
-  d.row = (kv_head(P.L, c.gi) << P.C.lg) + (pos & ((1 << P.C.lg) - 1));
-  d.mask = low_mask(c.n - pos) & (low_mask(P.L.sinks - pos) | ~low_mask(c.lo - pos));
+  d.pid = __ldg(c.pages + (pos >> P.C.lg));
+  d.row = c.kvrow + (pos & ((1 << P.C.lg) - 1));
+  d.mask = 0xffffu;
+  if (pos + 16 > c.n || pos < c.lo)                    // the end, the window's edges
+    d.mask = low_mask(c.n - pos) & (low_mask(P.L.sinks - pos) | ~low_mask(c.lo - pos));
   return d;
 }
 
@@ -382,6 +389,7 @@ struct PagedAttn {
   float m[2], l[2], mo[2];
   uint32_t q[8][2 * PagedCfg<KV>::kTerms];     // B fragments of Q^T, one pair per term
   float qf[2];                                 // e4m3: power of two taken out of the heads' query
+  float cf[2];                                 // e4m3: 2^(m - mo)
 };
 
 template <int KV>
@@ -391,7 +399,7 @@ __device__ __forceinline__ void attn_reset(PagedAttn<KV>& A) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) A.acc[i][e] = 0.f;
 #pragma unroll
-  for (int e = 0; e < 2; ++e) { A.m[e] = -INFINITY; A.mo[e] = -INFINITY; A.l[e] = 0.f; }
+  for (int e = 0; e < 2; ++e) { A.m[e] = A.mo[e] = -INFINITY; A.l[e] = 0.f; A.cf[e] = INFINITY; }
 }
 
 // (cos, sin) of the query position's 64 angles into this warp's table. theta lies in shared
@@ -513,7 +521,7 @@ __device__ __forceinline__ void paged_tile(PagedAttn<KV>& A, uint32_t stage, uin
   const int lane = threadIdx.x & 31, g = lane >> 2;
   const uint32_t tv = stage + 16 * Cfg::kRowB;
   float x[4];
-  float vs[2];
+  float vs[2] = {0.f, 0.f};
   if (KV == kKvBf16) {
     float s[3][4];
 #pragma unroll
@@ -563,29 +571,43 @@ __device__ __forceinline__ void paged_tile(PagedAttn<KV>& A, uint32_t stage, uin
     x[2] = (s[0][2] + s[1][2]) * (k1 * A.qf[0]);
     x[3] = (s[0][3] + s[1][3]) * (k1 * A.qf[1]);
   }
-  if (!((mask >> g) & 1u)) { x[0] = -INFINITY; x[1] = -INFINITY; }
-  if (!((mask >> (g + 8)) & 1u)) { x[2] = -INFINITY; x[3] = -INFINITY; }
+  if (mask != 0xffffu) {
+    if (!((mask >> g) & 1u)) { x[0] = x[1] = -INFINITY; vs[0] = 0.f; }
+    if (!((mask >> (g + 8)) & 1u)) { x[2] = x[3] = -INFINITY; vs[1] = 0.f; }
+  }
   float al[2] = {1.f, 1.f};
   const bool moved = move_ref(x, A.m, al);
   float p[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) p[e] = ex2_from(x[e], A.m[e & 1]);
+  {
+    const float m0 = A.m[0] == -INFINITY ? 0.f : A.m[0], m1 = A.m[1] == -INFINITY ? 0.f : A.m[1];
+    p[0] = ex2(x[0] - m0); p[1] = ex2(x[1] - m1);
+    p[2] = ex2(x[2] - m0); p[3] = ex2(x[3] - m1);
+  }
   if (moved) { A.l[0] *= al[0]; A.l[1] *= al[1]; }
   A.l[0] += p[0] + p[2];
   A.l[1] += p[1] + p[3];
   bool moved_o = moved;
   if (KV == kKvE4m3) {
-    // weights of the rows with their scales, against their own reference
-    const float lv0 = lg2(vs[0]), lv1 = lg2(vs[1]);
-    float y[4];
-    y[0] = (mask >> g) & 1u ? x[0] + lv0 : -INFINITY;
-    y[1] = (mask >> g) & 1u ? x[1] + lv0 : -INFINITY;
-    y[2] = (mask >> (g + 8)) & 1u ? x[2] + lv1 : -INFINITY;
-    y[3] = (mask >> (g + 8)) & 1u ? x[3] + lv1 : -INFINITY;
-    al[0] = al[1] = 1.f;
-    moved_o = move_ref(y, A.mo, al);
+    // The rows' weights with their scales, against their own reference: 2^(x + log2(vs) - mo) =
+    // p vs 2^(m - mo). A weight above 2^9 moves the reference; so does a factor above 2^64, whose
+    // p could have been too small a number.
+    if (moved) { A.cf[0] = ex2(A.m[0] - A.mo[0]); A.cf[1] = ex2(A.m[1] - A.mo[1]); }
+    const float f0 = vs[0] * A.cf[0], f1 = vs[0] * A.cf[1], f2 = vs[1] * A.cf[0], f3 = vs[1] * A.cf[1];
+    const float w0 = p[0] * f0, w1 = p[1] * f1, w2 = p[2] * f2, w3 = p[3] * f3;
+    const bool far = !((f0 + f1) + (f2 + f3) <= 1.8446744e19f) || !((w0 + w1) + (w2 + w3) <= 512.f);
+    moved_o = __any_sync(0xffffffffu, far);
+    if (moved_o) {
+      const float lv0 = lg2(vs[0]), lv1 = lg2(vs[1]);  // -inf for rows that are left out
+      const float y[4] = {x[0] + lv0, x[1] + lv0, x[2] + lv1, x[3] + lv1};
+      al[0] = al[1] = 1.f;
+      move_ref(y, A.mo, al);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) p[e] = ex2_from(y[e], A.mo[e & 1]);
+      for (int e = 0; e < 4; ++e) p[e] = ex2_from(y[e], A.mo[e & 1]);
+      A.cf[0] = ex2(A.m[0] - A.mo[0]);
+      A.cf[1] = ex2(A.m[1] - A.mo[1]);
+    } else {
+      p[0] = w0; p[1] = w1; p[2] = w2; p[3] = w3;
+    }
   } else {
     A.mo[0] = A.m[0];
     A.mo[1] = A.m[1];
