@@ -89,14 +89,11 @@ struct PagedSmem {
   static constexpr int kAng = kTheta + 64 * 8;                     // [warps][64] (cos, sin)
   static constexpr int kMask = kAng + Cfg::kWarps * 64 * 8;        // [warps][8] row masks
   static constexpr int kEnt = kMask + Cfg::kWarps * 8 * 4;
-  static constexpr int kList = kEnt + kEntries * (int)sizeof(PagedEntry);  // [warps][32] bytes
-  static constexpr int kPrefix = kList + Cfg::kWarps * 32;         // [129] line, [129] sequences
+  static constexpr int kPrefix = kEnt + kEntries * (int)sizeof(PagedEntry);   // [129] line, [129] sequences
   static constexpr int kMisc = kPrefix + 130 * 8 + 130 * 8;
   static constexpr int kWt = kMisc + 256;                          // [160][8] weights of a merge
   static constexpr int kBytes = kWt + kPagedMaxCTAs * 8 * 4;
-  // a drained ring: two partials, then [entries][8] weights of a merge
-  static constexpr int kEw = 2 * warp_part_floats(8) * 4;
-  static_assert(kEw + kEntries * 8 * 4 <= Cfg::kStages * Cfg::kStageB, "partials fit the ring");
+  static_assert(2 * warp_part_floats(8) * 4 <= Cfg::kStages * Cfg::kStageB, "a drained ring holds two partials");
 };
 
 // ------------------------------------------------------------------ conversions and products
@@ -242,6 +239,13 @@ __device__ __forceinline__ void cursor_next_group(const PagedDecodeParams& P, Cu
   }
   cursor_group(P, c);
 }
+// a / b for a quotient below 2^20: an estimate, off by one at most, and its correction
+__device__ __forceinline__ int small_div(int a, int b) {
+  int q = (int)(__fdividef((float)a, (float)b));
+  const int r = a - q * b;
+  return q + (r >= b) - (r < 0);
+}
+
 // The cursor of the first tile at or after a place of the line, rel places after the start of a
 // chunk of 32 sequences. lens: this lane's length of the chunk; incl and mine: its places with
 // and without the lanes before. *before: tiles of the line before that one, where seqs non-empty
@@ -263,12 +267,13 @@ __device__ __forceinline__ Cursor cursor_at(const PagedDecodeParams& P, int chun
   const int tr = ((c.n + 15) >> 4) + kSetup;
   int k;
   if (in_seq < P.L.n_ret * tr) {
-    c.gi = in_seq / tr;
+    c.gi = small_div(in_seq, tr);
     k = in_seq - c.gi * tr;
   } else {
     const int u = in_seq - P.L.n_ret * tr, tl = local_tiles(P.L, c.n).nt + kSetup;
-    c.gi = P.L.n_ret + u / tl;
-    k = u % tl;
+    c.gi = small_div(u, tl);
+    k = u - c.gi * tl;
+    c.gi += P.L.n_ret;
   }
   const long long groups = (long long)(seqs + __popc(live & ((1u << j) - 1))) * P.L.Hkv + c.gi;
   *before = place - groups * kSetup - min(k, kSetup);
@@ -1026,88 +1031,64 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams P) {
     }
   }
   __syncthreads();
+  auto entry_part = [&](int j) {
+    return reinterpret_cast<const float*>(sm + (j >> 1) * NS * Cfg::kStageB) + (j & 1) * warp_part_floats(G);
+  };
 
   // ---- the open ends of this CTA's warps: the entries of a group (a run) are merged in the order
-  // of the line, its heads shared out among NW / runs warps
+  // of the line, one (run, head) a warp. (The code is kept small: it runs once, and most of its
+  // time is that of fetching its instructions.)
   int open_run[2] = {-1, -1};                          // first entry of the groups left open
   {
-    float* ew = reinterpret_cast<float*>(ring + S::kEw);
-    unsigned char* list = sm + S::kList + warp * 32;
     const int gid = lane < 2 * NW ? ent[lane].gid : -1;
-    uint32_t same = 0;                                 // (a match instruction took 1000 cycles a value)
-#pragma unroll
-    for (int i = 0; i < 2 * NW; ++i) same |= (uint32_t)(__shfl_sync(0xffffffffu, gid, i) == gid) << i;
-    const bool lead = gid >= 0 && __ffs(same) - 1 == lane;
-    uint32_t leads = __ballot_sync(0xffffffffu, lead);
+    const uint32_t valid = __ballot_sync(0xffffffffu, gid >= 0), below = valid & ((1u << lane) - 1);
+    const int before = __shfl_sync(0xffffffffu, gid, below ? 31 - __clz(below) : 0);
+    const bool lead = gid >= 0 && (!below || before != gid);
+    const uint32_t leads = __ballot_sync(0xffffffffu, lead);
     const uint32_t left = __ballot_sync(0xffffffffu, lead && ent[lane & (2 * NW - 1)].gs < ct0);
-    const uint32_t right = __ballot_sync(0xffffffffu, lead && ent[lane & (2 * NW - 1)].ge > ct1);
+    const uint32_t right = __ballot_sync(0xffffffffu, lead && ent[lane & (2 * NW - 1)].ge > ct1) & ~left;
     if (left) open_run[0] = __ffs(left) - 1;
-    if (right & ~left) open_run[1] = __ffs(right & ~left) - 1;
-    const int n_runs = __popc(leads);
-    const int share = max(1, NW / max(n_runs, 1));     // warps of a run
-    const int teams = NW / share, team = warp / share;
-    for (int r = 0; leads; ++r, leads &= leads - 1) {
-      if (r % teams != team) continue;
-      const int first = __ffs(leads) - 1;
-      const uint32_t members = __shfl_sync(0xffffffffu, same, first);
-      const int cnt = __popc(members);
-      __syncwarp();
-      if ((members >> lane) & 1u) list[__popc(members & ((1u << lane) - 1))] = lane;
-      __syncwarp();
-      auto part_of = [&](int i) {
-        const int j = list[i];
-        return reinterpret_cast<const float*>(sm + (j >> 1) * NS * Cfg::kStageB) +
-               (j & 1) * warp_part_floats(G);
-      };
-      // head lane % 8 over entries lane / 8, lane / 8 + 4, ...
-      const int h8 = lane & 7;
-      float M = -INFINITY, MO = -INFINITY, Ls = 0.f;
-      if (h8 < G)
-        for (int i = lane >> 3; i < cnt; i += 4) {
-          const float* q = part_of(i) + G * kPartPitch + 3 * h8;
+    if (right) open_run[1] = __ffs(right) - 1;
+    int unit = 0;
+#pragma unroll 1
+    for (uint32_t todo = leads; todo; unit += G) {
+      const int first = __ffs(todo) - 1;
+      uint32_t members = valid & ~((1u << first) - 1);
+      todo &= todo - 1;
+      if (todo) members &= (1u << (__ffs(todo) - 1)) - 1;
+#pragma unroll 1
+      for (int h = (warp - unit) & (NW - 1); h < G; h += NW) {
+        float M = -INFINITY, MO = -INFINITY, Ls = 0.f;
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (uint32_t mem = members; mem; mem &= mem - 1) {
+          const float* q = entry_part(__ffs(mem) - 1) + G * kPartPitch + 3 * h;
           M = fmaxf(M, q[0]);
           MO = fmaxf(MO, q[2]);
         }
-#pragma unroll
-      for (int o = 8; o < 32; o <<= 1) {
-        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        MO = fmaxf(MO, __shfl_xor_sync(0xffffffffu, MO, o));
-      }
-      if (h8 < G)
-        for (int i = lane >> 3; i < cnt; i += 4) {
-          const float* q = part_of(i) + G * kPartPitch + 3 * h8;
+#pragma unroll 1
+        for (uint32_t mem = members; mem; mem &= mem - 1) {
+          const float* q = entry_part(__ffs(mem) - 1);
+          const float4 a = *reinterpret_cast<const float4*>(q + h * kPartPitch + 4 * lane);
+          q += G * kPartPitch + 3 * h;
+          const float w = ex2_from(q[2], MO);
           Ls += q[1] * ex2_from(q[0], M);
-          ew[i * 8 + h8] = ex2_from(q[2], MO);
-        }
-#pragma unroll
-      for (int o = 8; o < 32; o <<= 1) Ls += __shfl_xor_sync(0xffffffffu, Ls, o);
-      __syncwarp();
-      const float f = Ls > 0.f || Ls != Ls ? ex2_from(MO, M) / Ls : 0.f;
-      const bool whole = first != open_run[0] && first != open_run[1];
-      const int gd = ent[first].gid, b = gd / L.Hkv;
-      const int64_t head0 = (int64_t)b * L.Hq + (int64_t)kv_head(L, gd - b * L.Hkv) * G;
-      float* gp = P.part + (int64_t)(blockIdx.x * 2 + (first == open_run[0] ? 0 : 1)) * cta_part_floats(G);
-      for (int h = warp % share; h < G; h += share) {
-        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int i = 0; i < cnt; ++i) {
-          const float4 a = *reinterpret_cast<const float4*>(part_of(i) + h * kPartPitch + 4 * lane);
-          const float w = ew[i * 8 + h];
           s.x = fmaf(a.x, w, s.x); s.y = fmaf(a.y, w, s.y);
           s.z = fmaf(a.z, w, s.z); s.w = fmaf(a.w, w, s.w);
         }
-        if (whole) {
-          const float fh = __shfl_sync(0xffffffffu, f, h);
+        if (first != open_run[0] && first != open_run[1]) {
+          const int gd = ent[first].gid, b = small_div(gd, L.Hkv);
+          const int64_t head = (int64_t)b * L.Hq + (int64_t)kv_head(L, gd - b * L.Hkv) * G + h;
+          const float f = Ls > 0.f || Ls != Ls ? ex2_from(MO, M) / Ls : 0.f;
           uint2 w;
-          w.x = pack_bf2(s.x * fh, s.y * fh);
-          w.y = pack_bf2(s.z * fh, s.w * fh);
-          *reinterpret_cast<uint2*>(P.out + (head0 + h) * kD + 4 * lane) = w;
-          if (P.lse && lane == h) P.lse[head0 + h] = (M + log2f(Ls)) * 0.6931471805599453f;
+          w.x = pack_bf2(s.x * f, s.y * f);
+          w.y = pack_bf2(s.z * f, s.w * f);
+          *reinterpret_cast<uint2*>(P.out + head * kD + 4 * lane) = w;
+          if (P.lse && lane == 0) P.lse[head] = (M + log2f(Ls)) * 0.6931471805599453f;
         } else {
+          float* gp = P.part + (int64_t)(blockIdx.x * 2 + (first == open_run[0] ? 0 : 1)) * cta_part_floats(G);
           *reinterpret_cast<float4*>(gp + h * kD + 4 * lane) = s;
-          if (lane == h) {
-            gp[G * kD + 3 * h] = M; gp[G * kD + 3 * h + 1] = Ls; gp[G * kD + 3 * h + 2] = MO;
-          }
+          if (lane < 3) gp[G * kD + 3 * h + lane] = lane == 0 ? M : lane == 1 ? Ls : MO;
         }
       }
     }
@@ -1141,20 +1122,21 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams P) {
     const int c0 = range_of(split, e.gs), np = range_of(split, e.ge - 1) - c0 + 1;
     // part i: the open end of CTA c0 + i (its last group for i = 0, its first otherwise)
     const float* part = P.part + (int64_t)c0 * 2 * pf;
-    const int b = e.gid / L.Hkv;
+    const int b = small_div(e.gid, L.Hkv);
     const int64_t head0 = (int64_t)b * L.Hq + (int64_t)kv_head(L, e.gid - b * L.Hkv) * G;
-    // four channels a thread; where G is small, teams of threads share out the parts. The first
-    // parts are on their way while the weights are made.
-    constexpr int kAhead = 4;
+    // Four channels a thread; where G is small, teams of threads share out the parts.
+    // As many parts as the rings hold are copied to shared memory, all copies in flight at once
+    // (loads into registers, 8 at a time, took 9 us for 103 parts), while the weights are made.
+    const int pb = (int)pf * 4, fit = S::kRing / pb;
+    const unsigned char* part_b = reinterpret_cast<const unsigned char*>(part);
     const int teams = NT / items, team = tid / items, it = tid - team * items, h = it >> 5;
-    float4 ahead[kAhead];
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int i = team + u * teams;
-      ahead[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (team < teams && i < np)
-        ahead[u] = __ldcg(reinterpret_cast<const float4*>(part + (i * 2 + (i == 0)) * pf) + it);
-    }
+    auto copy = [&](int i0, int nb) {                  // a thread copies the 16 bytes it sums up
+      if (team < teams)
+        for (int i = i0 + team; i < i0 + nb; i += teams)
+          cp_async16(sm + (i - i0) * pb + it * 16, part_b + (int64_t)(i * 2 + (i == 0)) * pb + it * 16);
+      cp_async_commit();
+    };
+    copy(0, min(np, fit));
     if (warp < G) {
       float m[kPagedMaxCTAs / 32], l[kPagedMaxCTAs / 32], mo[kPagedMaxCTAs / 32];
       float M = -INFINITY, MO = -INFINITY, Ls = 0.f;
@@ -1188,21 +1170,26 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams P) {
         if (P.lse) P.lse[head0 + warp] = (M + log2f(Ls)) * 0.6931471805599453f;
       }
     }
-    __syncthreads();
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](const float4& a, int i) {
-      const float w = wt[i * 8 + h];
-      s.x = fmaf(a.x, w, s.x); s.y = fmaf(a.y, w, s.y);
-      s.z = fmaf(a.z, w, s.z); s.w = fmaf(a.w, w, s.w);
-    };
-    if (team < teams) {
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u)
-        if (team + u * teams < np) add(ahead[u], team + u * teams);
-#pragma unroll 8
-      for (int i = team + kAhead * teams; i < np; i += teams)
-        add(__ldcg(reinterpret_cast<const float4*>(part + (i * 2 + (i == 0)) * pf) + it), i);
+    for (int i0 = 0; i0 < np; i0 += fit) {
+      if (i0 > 0) {
+        __syncthreads();
+        copy(i0, min(np - i0, fit));
+      }
+      cp_async_wait<0>();
+      __syncthreads();
+      if (team < teams) {
+        const int end = min(np, i0 + fit);
+#pragma unroll 4
+        for (int i = i0 + team; i < end; i += teams) {
+          const float4 a = *reinterpret_cast<const float4*>(sm + (i - i0) * pb + it * 16);
+          const float w = wt[i * 8 + h];
+          s.x = fmaf(a.x, w, s.x); s.y = fmaf(a.y, w, s.y);
+          s.z = fmaf(a.z, w, s.z); s.w = fmaf(a.w, w, s.w);
+        }
+      }
     }
+    __syncthreads();
     float4* red = reinterpret_cast<float4*>(sm);
     red[tid] = s;
     __syncthreads();
