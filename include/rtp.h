@@ -232,7 +232,7 @@ enum {
 typedef struct {
   int32_t kv_type;        /* RTP_KV_* */
   int32_t page_size;      /* tokens per page: 16, 32, 64, 128 or 256 */
-  int32_t n_pages;        /* n_pages * page_size <= 2^31 - 1 */
+  int32_t n_pages;        /* n_pages * page_size and n_pages * page_stride <= 2^31 - 1 */
   int32_t table_stride;   /* entries per row of block_table, >= 1 */
   void* k;                /* [n_pages][Hkv][page_size][128]: RoPE'd keys */
   void* v;                /* [n_pages][Hkv][page_size][128]: values */

@@ -581,12 +581,14 @@ int check_paged(const rtp_paged_cache* c, int Hkv, PagedPtrs& C) {
   if (((int64_t)c->n_pages << lg) > 0x7fffffffLL) return RTP_ESHAPE;    // slots are int32
   const int64_t block = (int64_t)Hkv << lg;
   if (c->page_stride != 0 && c->page_stride < block) return RTP_ESHAPE;
+  const int64_t stride = c->page_stride ? c->page_stride : block;
+  if (stride > 0x7fffffffLL / c->n_pages) return RTP_ESHAPE;            // so are row numbers
   C.k = static_cast<unsigned char*>(c->k);
   C.v = static_cast<unsigned char*>(c->v);
   C.ks = c->k_scale;
   C.vs = c->v_scale;
   C.table = c->block_table;
-  C.page_stride = c->page_stride ? c->page_stride : block;
+  C.page_stride = (int)stride;
   C.table_stride = c->table_stride;
   C.n_pages = c->n_pages;
   C.lg = lg;
@@ -603,9 +605,10 @@ int launch_paged(const PagedDecodeParams& P, const DevInfo& di, cudaStream_t st)
   });
   if (rc != 0) return RTP_ECUDA;
   constexpr int nw = PagedCfg<KV>::kWarps;
-  // no more CTAs than the longest lengths could give a tile per warp
+  // no more CTAs than the longest lengths could give a tile per warp, or a group each
   const int64_t most = (int64_t)P.L.B * P.L.Hkv * ((P.L.maxN + 15) / 16);
-  const int grid = (int)std::min<int64_t>(std::min(di.sms, kPagedMaxCTAs), (most + nw - 1) / nw);
+  const int64_t want = std::max<int64_t>((most + nw - 1) / nw, (int64_t)P.L.B * P.L.Hkv);
+  const int grid = (int)std::min<int64_t>(std::min(di.sms, kPagedMaxCTAs), want);
   paged_decode_kernel<KV, APPEND><<<grid, nw * 32, smem, st>>>(P);
   g_launches = 1;
   return cudaGetLastError() == cudaSuccess ? RTP_OK : RTP_ECUDA;
@@ -732,15 +735,12 @@ int rtp_paged_append_kv(const rtp_layer_desc* desc, const rtp_paged_cache* cache
   const dim3 grid((unsigned)gx, groups);
   const int smem = 4 * r * (1024 + heads * 512);       // at most 40 KB
   cudaStream_t st = (cudaStream_t)stream;
-  if (cache->kv_type == RTP_KV_BF16) {
-    if (r == 1) paged_append_kernel<kKvBf16, 1><<<grid, 256, smem, st>>>(P);
-    else if (r == 2) paged_append_kernel<kKvBf16, 2><<<grid, 256, smem, st>>>(P);
-    else paged_append_kernel<kKvBf16, 4><<<grid, 256, smem, st>>>(P);
-  } else {
-    if (r == 1) paged_append_kernel<kKvE4m3, 1><<<grid, 256, smem, st>>>(P);
-    else if (r == 2) paged_append_kernel<kKvE4m3, 2><<<grid, 256, smem, st>>>(P);
-    else paged_append_kernel<kKvE4m3, 4><<<grid, 256, smem, st>>>(P);
-  }
+  auto kernel = r == 1 ? paged_append_kernel<kKvBf16, 1>
+                : r == 2 ? paged_append_kernel<kKvBf16, 2> : paged_append_kernel<kKvBf16, 4>;
+  if (cache->kv_type == RTP_KV_E4M3)
+    kernel = r == 1 ? paged_append_kernel<kKvE4m3, 1>
+             : r == 2 ? paged_append_kernel<kKvE4m3, 2> : paged_append_kernel<kKvE4m3, 4>;
+  kernel<<<grid, 256, smem, st>>>(P);
   g_launches = 1;
   return cudaGetLastError() == cudaSuccess ? RTP_OK : RTP_ECUDA;
 }

@@ -32,7 +32,7 @@ struct PagedPtrs {
   unsigned char *k, *v;          // [n_pages] pages of [Hkv][page][128], page_stride rows apart
   float *ks, *vs;                // e4m3: [n_pages][Hkv][page]
   const int32_t* table;          // [B][table_stride]
-  int64_t page_stride;           // rows
+  int page_stride;               // rows; all rows are below 2^31
   int table_stride, n_pages, lg; // page = 1 << lg
 };
 
@@ -54,7 +54,7 @@ template <> struct PagedCfg<kKvBf16> {
   static constexpr int kStageB = 16 * 512;
 };
 template <> struct PagedCfg<kKvE4m3> {
-  static constexpr int kWarps = 16, kStages = 3, kRowB = 128, kTerms = 2;
+  static constexpr int kWarps = 12, kStages = 4, kRowB = 128, kTerms = 2;
   static constexpr int kStageB = 16 * 256 + 128;
 };
 
@@ -62,7 +62,7 @@ template <> struct PagedCfg<kKvE4m3> {
 constexpr int kPagedMaxWarps = 16;
 // Tiles' worth of a group's fixed cost (query, angles, output) in the split of the line
 constexpr int kSetup = 3;
-static_assert(kSetup > 0, "an empty sequence at the end of the line is divided by it");
+static_assert(kSetup > 0, "an empty sequence is divided by its places");
 
 // floats of a warp's partial (rows of 132: the accumulators' lanes hit all banks) and of a CTA's
 constexpr int kPartPitch = 132;
@@ -79,6 +79,9 @@ struct PagedEntry {              // an open end of a warp's range
   int pad;
 };
 
+// Tiles per warp up to which a group stays in one CTA, where every group can have one
+constexpr int kOneCta = 5;
+
 template <int KV>
 struct PagedSmem {
   using Cfg = PagedCfg<KV>;
@@ -89,8 +92,8 @@ struct PagedSmem {
   static constexpr int kAng = kTheta + 64 * 8;                     // [warps][64] (cos, sin)
   static constexpr int kMask = kAng + Cfg::kWarps * 64 * 8;        // [warps][8] row masks
   static constexpr int kEnt = kMask + Cfg::kWarps * 8 * 4;
-  static constexpr int kPrefix = kEnt + kEntries * (int)sizeof(PagedEntry);   // [129] line, [129] sequences
-  static constexpr int kMisc = kPrefix + 130 * 8 + 130 * 8;
+  static constexpr int kPrefix = kEnt + kEntries * (int)sizeof(PagedEntry);   // [129]
+  static constexpr int kMisc = kPrefix + 130 * 8;
   static constexpr int kWt = kMisc + 256;                          // [160][8] weights of a merge
   static constexpr int kBytes = kWt + kPagedMaxCTAs * 8 * 4;
   static_assert(2 * warp_part_floats(8) * 4 <= Cfg::kStages * Cfg::kStageB, "a drained ring holds two partials");
@@ -247,20 +250,13 @@ __device__ __forceinline__ int small_div(int a, int b) {
 }
 
 // The cursor of the first tile at or after a place of the line, rel places after the start of a
-// chunk of 32 sequences. lens: this lane's length of the chunk; incl and mine: its places with
-// and without the lanes before. *before: tiles of the line before that one, where seqs non-empty
-// sequences lie before the chunk; *first: its place.
-__device__ __forceinline__ Cursor cursor_at(const PagedDecodeParams& P, int chunk, long long place,
-                                            long long base, int seqs, int lens, long long incl,
-                                            long long mine, long long* before,
-                                            long long* first) {
+// chunk of 32 sequences (not at its end). lens: this lane's length of the chunk; incl and mine: its
+// places with and without the lanes before. *skip: places from there to the tile.
+__device__ __forceinline__ Cursor cursor_at(const PagedDecodeParams& P, int chunk, long long rel,
+                                            int lens, long long incl, long long mine, int* skip) {
   Cursor c;
-  const long long rel = place - base;
   c.lens = lens;
-  // (the end of the line, past the last sequence, has no tile; its count of tiles is right)
-  const uint32_t done = __ballot_sync(0xffffffffu, incl <= rel);
-  const uint32_t live = __ballot_sync(0xffffffffu, lens > 0);
-  const int j = min(__popc(done), 31);
+  const int j = __popc(__ballot_sync(0xffffffffu, incl <= rel)) & 31;
   c.b = chunk * 32 + j;
   c.n = __shfl_sync(0xffffffffu, lens, j);
   const int in_seq = (int)(rel - __shfl_sync(0xffffffffu, incl - mine, j));
@@ -275,18 +271,25 @@ __device__ __forceinline__ Cursor cursor_at(const PagedDecodeParams& P, int chun
     k = u - c.gi * tl;
     c.gi += P.L.n_ret;
   }
-  const long long groups = (long long)(seqs + __popc(live & ((1u << j) - 1))) * P.L.Hkv + c.gi;
-  *before = place - groups * kSetup - min(k, kSetup);
-  *first = place + max(kSetup - k, 0);
+  *skip = max(kSetup - k, 0);
   c.k = max(k - kSetup, 0);
   cursor_group(P, c);
   return c;
 }
-__device__ __forceinline__ long long warp_incl_sum(long long x) {
+// The next tile, and its place
+__device__ __forceinline__ void cursor_step(const PagedDecodeParams& P, Cursor& c, int& place) {
+  ++place;
+  if (++c.k == c.nt) {
+    cursor_next_group(P, c);
+    place += kSetup;
+  }
+}
+template <class I>
+__device__ __forceinline__ I warp_incl_sum(I x) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long u = __shfl_up_sync(0xffffffffu, x, o);
+    const I u = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += u;
   }
   return x;
@@ -295,18 +298,14 @@ __device__ __forceinline__ long long warp_incl_sum(long long x) {
 // The line cut into n <= 160 ranges, the first `extra` of them one place longer. Plain 64-bit
 // divisions cost about 500 cycles each here; there is one left, for lines beyond 2^32 places.
 struct LineSplit {
-  long long each, T;
+  long long each;
   int n, extra;
-  float inv, inv1;
 };
 __device__ __forceinline__ LineSplit split_line(long long T, int n) {
   LineSplit s;
-  s.T = T;
   s.n = n;
   s.each = T >> 32 ? T / n : (long long)((uint32_t)T / (uint32_t)n);
   s.extra = (int)(T - s.each * n);
-  s.inv = 1.f / (float)s.each;
-  s.inv1 = 1.f / (float)(s.each + 1);
   return s;
 }
 __device__ __forceinline__ long long range_start(const LineSplit& s, int i) {
@@ -315,9 +314,9 @@ __device__ __forceinline__ long long range_start(const LineSplit& s, int i) {
 // The range that holds a place: the quotient is below 160, so its single-precision estimate is
 // off by one at most.
 __device__ __forceinline__ int range_of(const LineSplit& s, long long place) {
-  int i = min((int)((float)place * s.inv1), s.n - 1);
+  int i = min((int)__fdividef((float)place, (float)(s.each + 1)), s.n - 1);
   if (i >= s.extra)
-    i = min(s.extra + (int)((float)(place - s.extra * (s.each + 1)) * s.inv), s.n - 1);
+    i = min(s.extra + (int)__fdividef((float)(place - s.extra * (s.each + 1)), (float)s.each), s.n - 1);
   if (range_start(s, i) > place) --i;
   if (i + 1 < s.n && range_start(s, i + 1) <= place) ++i;
   return i;
@@ -345,14 +344,14 @@ __device__ __forceinline__ void tile_issue(const PagedDecodeParams& P, const Til
   using Cfg = PagedCfg<KV>;
   const int lane = threadIdx.x & 31;
   uint32_t mask = d.mask;
-  int64_t pid = d.pid;
-  if ((uint32_t)d.pid >= (uint32_t)P.C.n_pages) {      // a page that does not exist: no rows
+  int pid = d.pid;
+  if ((uint32_t)pid >= (uint32_t)P.C.n_pages) {        // a page that does not exist: no rows
     if (lane == 0) set_status(P.status, -6);
     mask = 0;
     pid = 0;
   }
   if (lane == 0) *mask_slot = mask;
-  const int64_t off = (pid * P.C.page_stride + d.row) * Cfg::kRowB + lane * 16;
+  const int64_t off = (int64_t)(pid * P.C.page_stride + d.row) * Cfg::kRowB + lane * 16;
   const unsigned char* kp = P.C.k + off;
   const unsigned char* vp = P.C.v + off;
   constexpr int kCh = Cfg::kRowB / 16;                 // chunks per row: 16 or 8
@@ -377,8 +376,7 @@ __device__ __forceinline__ void tile_issue(const PagedDecodeParams& P, const Til
     }
   }
   if (KV == kKvE4m3 && lane < 8) {                     // 16 scales of K, then of V
-    const float* sp = (lane < 4 ? P.C.ks : P.C.vs) +
-                      pid * ((int64_t)P.L.Hkv << P.C.lg) + d.row + (lane & 3) * 4;
+    const float* sp = (lane < 4 ? P.C.ks : P.C.vs) + (pid * (P.L.Hkv << P.C.lg) + d.row + (lane & 3) * 4);
     cp_async16_s(stage + 32 * Cfg::kRowB + lane * 16, sp);
   }
 }
@@ -553,9 +551,12 @@ __device__ __forceinline__ void paged_tile(PagedAttn<KV>& A, uint32_t stage, uin
     const int r = lane & 15;
     const uint32_t ka = stage + r * 128 + (uint32_t)(((lane >> 4) ^ (r & 7)) << 4);
 #pragma unroll
+    uint32_t wk[4][4];                                 // (all loads first: 6 % on the whole step)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ldsm_x4(ka ^ (uint32_t)(i << 5), wk[i]);
+#pragma unroll
     for (int i = 0; i < 4; ++i) {
-      uint32_t w[4];
-      ldsm_x4(ka ^ (uint32_t)(i << 5), w);
+      uint32_t (&w)[4] = wk[i];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const uint32_t a[4] = {e4m3x2_h2(w[2 * c]), e4m3x2_h2(w[2 * c + 1]),
@@ -845,99 +846,115 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams P) {
   // ---- the line: places before each 32 sequences, and in all. Up to 32 sequences: every warp
   // makes the sums itself.
   const int nc = (L.B + 31) >> 5;
-  long long* seqs_before = prefix + 130;
-  int lens = 0, chunk = 0, seqs = 0;
+  int lens = 0, chunk = 0;
   long long mine = 0, incl = 0, base = 0, T;
   if (tid < 2 * NW) ent[tid].gid = -1;
   bool bad = false;
   if (nc == 1) lens = paged_len(P, lane, &bad);
   if (lane == 0) {                                     // while the lengths are on their way
 #pragma unroll
-    for (int i = 0; i < kD / 2 / NW; ++i) theta[warp * (kD / 2 / NW) + i] = L.theta[warp * (kD / 2 / NW) + i];
+    for (int i = 0; i < (kD / 2 + NW - 1) / NW; ++i)
+      if (warp + i * NW < kD / 2) theta[warp + i * NW] = L.theta[warp + i * NW];
   }
   if (nc == 1) {
-    mine = seq_places(L, lens);
-    incl = warp_incl_sum(mine);
-    T = __shfl_sync(0xffffffffu, incl, 31);
+    const uint32_t m = (uint32_t)seq_places(L, lens), in = warp_incl_sum(m);   // below 2^32
+    mine = m;
+    incl = in;
+    T = __shfl_sync(0xffffffffu, in, 31);
     if (warp == 0) paged_idle(P, 0, lens, bad);
   } else {
     for (int ch = warp; ch < nc; ch += NW) {
       bad = false;
       const int n = paged_len(P, ch * 32 + lane, &bad);
       const long long t = warp_incl_sum(seq_places(L, n));
-      const uint32_t live = __ballot_sync(0xffffffffu, n > 0);
-      if (lane == 31) { prefix[ch] = t; seqs_before[ch] = __popc(live); }
+      if (lane == 31) prefix[ch] = t;
       paged_idle(P, ch, n, bad);
     }
     __syncthreads();
-    if (warp < 2) {                                    // exclusive sums, the total at [nc]
-      long long* x = warp ? seqs_before : prefix;
+    if (warp == 0) {                                   // exclusive sums, the total at [nc]
       long long run = 0;
       for (int c0 = 0; c0 < nc; c0 += 32) {
-        const long long m = c0 + lane < nc ? x[c0 + lane] : 0;
+        const long long m = c0 + lane < nc ? prefix[c0 + lane] : 0;
         const long long in = warp_incl_sum(m);
-        if (c0 + lane < nc) x[c0 + lane] = run + in - m;
+        if (c0 + lane < nc) prefix[c0 + lane] = run + in - m;
         run += __shfl_sync(0xffffffffu, in, 31);
       }
-      if (lane == 0) x[nc] = run;
+      if (lane == 0) prefix[nc] = run;
     }
     __syncthreads();
     T = prefix[nc];
   }
-  // CTAs that take part: at least one place per warp
   if (T == 0) return;
-  // CTAs: all, as far as each warp gets a place. With few sequences a group's parts are what
-  // counts in the end: spread over c CTAs, a group of x tiles takes a warp x / (c NW) tiles of
-  // 0.8 us, and the CTA that joins it c parts of 13 ns a head; best at c^2 = 64 x / (NW G).
-  int ctas = gridDim.x;
-  if (T < (long long)ctas * NW) ctas = ((int)T + NW - 1) / NW;
-  if (nc == 1 && T < (1 << 20)) {
-    const int x = __reduce_max_sync(0xffffffffu, L.n_ret ? (lens + 15) >> 4 : local_tiles(L, lens).nt);
-    ctas = min(ctas, (int)(sqrtf(64.f / (NW * G) / (float)x) * (float)T) + 1);
-  }
-  const LineSplit split = split_line(T, ctas);
-  if (blockIdx.x >= split.n) return;
-  const long long ct0 = range_start(split, blockIdx.x), ct1 = range_start(split, blockIdx.x + 1);
-  const int len = (int)(ct1 - ct0);                    // below 2^31: a sequence has 2^26 places at most
-  const long long p0 = ct0 + (int)((long long)warp * len / NW);
-  const long long p1 = ct0 + (int)((long long)(warp + 1) * len / NW);
-  Cursor cc;
-  long long line;                                      // place of the tile at cc
-  int n = 0;                                           // tiles of this warp
+  // ---- this CTA's range
+  long long ct0, ct1;
+  LineSplit split;
   {
-    long long tiles[2];
-#pragma unroll
-    for (int e = 1; e >= 0; --e) {                     // the end, then the start (which stays in cc)
-      const long long p = e ? p1 : p0;
-      if (nc > 1) {
-        int before = 0;                                // chunks that start at or before p
-        for (int i = lane; i < nc; i += 32) before += prefix[i] <= p;
-        chunk = __reduce_add_sync(0xffffffffu, before) - 1;
-        base = prefix[chunk];
-        seqs = (int)seqs_before[chunk];
-        lens = paged_len(P, chunk * 32 + lane, nullptr);
-        mine = seq_places(L, lens);
-        incl = warp_incl_sum(mine);
-      }
-      cc = cursor_at(P, chunk, p, base, seqs, lens, incl, mine, &tiles[e], &line);
+    const uint32_t live = __ballot_sync(0xffffffffu, lens > 0);
+    const int x = nc > 1 ? 0 : __reduce_max_sync(0xffffffffu, L.n_ret ? (lens + 15) >> 4 : local_tiles(L, lens).nt);
+    if (nc == 1 && x <= kOneCta * NW && __popc(live) * L.Hkv <= gridDim.x) {
+      // Few short groups: one CTA each. Joining the parts of several CTAs takes 4 us, as much as
+      // 5 tiles of a warp.
+      if (blockIdx.x >= __popc(live) * L.Hkv) return;
+      const int s = small_div(blockIdx.x, L.Hkv), gi = blockIdx.x - s * L.Hkv;
+      const int j = __ffs(__ballot_sync(0xffffffffu, lens > 0 && __popc(live & ((1u << lane) - 1)) == s)) - 1;
+      const int n = __shfl_sync(0xffffffffu, lens, j), tr = ((n + 15) >> 4) + kSetup;
+      const int tl = local_tiles(L, n).nt + kSetup;
+      ct0 = __shfl_sync(0xffffffffu, incl - mine, j) + min(gi, L.n_ret) * tr + max(gi - L.n_ret, 0) * tl;
+      ct1 = ct0 + (gi < L.n_ret ? tr : tl);
+      // (no split: no group is left open); the places without a tile would leave warps idle
+      ct0 += kSetup;
+    } else {
+      // All CTAs, as far as each warp gets a place. With few sequences a group's parts are what
+      // counts in the end: spread over c CTAs, a group of x tiles takes a warp x / (c NW) tiles of
+      // 0.8 us, and the CTA that joins it c parts of 13 ns a head; best at c^2 = 64 x / (NW G).
+      int ctas = gridDim.x;
+      if (T < (long long)ctas * NW) ctas = ((int)T + NW - 1) / NW;
+      if (nc == 1 && T < (1 << 20))
+        ctas = min(ctas, (int)(sqrtf(64.f / (NW * G) / (float)x) * (float)T) + 1);
+      split = split_line(T, ctas);
+      if (blockIdx.x >= split.n) return;
+      ct0 = range_start(split, blockIdx.x);
+      ct1 = range_start(split, blockIdx.x + 1);
     }
-    n = (int)(tiles[1] - tiles[0]);
+  }
+  const int len = (int)(ct1 - ct0);                    // below 2^31: a sequence has 2^26 places at most
+  // this warp's places, counted from ct0
+  int line = (int)((long long)warp * len / NW);        // place of the tile at cc
+  const int p1 = (int)((long long)(warp + 1) * len / NW);
+  Cursor cc;
+  if (line < p1) {
+    const long long p0 = ct0 + line;
+    if (nc > 1) {
+      int before = 0;                                  // chunks that start at or before p0
+      for (int i = lane; i < nc; i += 32) before += prefix[i] <= p0;
+      chunk = __reduce_add_sync(0xffffffffu, before) - 1;
+      base = prefix[chunk];
+      lens = paged_len(P, chunk * 32 + lane, nullptr);
+      mine = seq_places(L, lens);
+      incl = warp_incl_sum(mine);
+    }
+    int skip;
+    cc = cursor_at(P, chunk, p0 - base, lens, incl, mine, &skip);
+    line += skip;
   }
   __syncthreads();                                     // theta, ent
 
   unsigned char* ring = sm + warp * NS * Cfg::kStageB;
   const uint32_t ring_s = smem_u32(ring);
   PagedAttn<KV> A;
-  if (n > 0) {
+  if (line < p1) {
     Cursor pc = cc;
+    int pline = line;                                  // place of the tile at pc, the next to copy
     // fill the ring: the page ids of its tiles are loaded together, and the first query and its
     // angles meanwhile
     TileDesc d[NS];
+    bool have[NS];
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
-      if (s < n) {
+      have[s] = pline < p1;
+      if (have[s]) {
         d[s] = tile_desc(P, pc);
-        if (++pc.k == pc.nt) cursor_next_group(P, pc);
+        cursor_step(P, pc, pline);
       }
     }
     QueryRaw qr;
@@ -945,22 +962,23 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams P) {
     fill_angles(theta, ang, cc.n - 1);
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
-      if (s < n) tile_issue<KV>(P, d[s], ring_s + s * Cfg::kStageB, masks + s);
+      if (have[s]) tile_issue<KV>(P, d[s], ring_s + s * Cfg::kStageB, masks + s);
       cp_async_commit();
     }
     TileDesc nx;                                       // the next tile, its page id on the way
-    if (NS < n) {
+    bool more = pline < p1;
+    if (more) {
       nx = tile_desc(P, pc);
-      if (++pc.k == pc.nt) cursor_next_group(P, pc);
+      cursor_step(P, pc, pline);
     }
     query_terms<KV>(A, qr, ang, G);
     attn_reset<KV>(A);
     int seg_k = cc.k, ang_b = cc.b, slot = 0;
-    bool has_head = false;
+    bool has_head = false, fresh = false;
 #pragma unroll 1
-    for (int i = 0; i < n; ++i) {
+    while (line < p1) {
       const int kvh = kv_head(L, cc.gi);
-      if (cc.k == 0 && i > 0) {                        // first tile of a group
+      if (fresh) {                                     // first tile of a group
         QueryRaw q2;
         query_fetch<KV>(P, q2, cc.b, kvh);
         if (cc.b != ang_b) {
@@ -970,6 +988,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams P) {
         query_terms<KV>(A, q2, ang, G);
         attn_reset<KV>(A);
         seg_k = 0;
+        fresh = false;
       }
       cp_async_wait<NS - 1>();
       __syncwarp();
@@ -977,18 +996,19 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams P) {
       const uint32_t mask = masks[slot];
       if (APPEND && cc.k == cc.nt - 1 && mask) {       // the last tile holds the new token's row
         const int pos = cc.n - 1;
-        const int64_t pid = __ldg(P.C.table + (int64_t)cc.b * P.C.table_stride + (pos >> P.C.lg));
-        const int64_t in = ((int64_t)kvh << P.C.lg) + (pos & ((1 << P.C.lg) - 1));
+        const int pid = __ldg(P.C.table + (int64_t)cc.b * P.C.table_stride + (pos >> P.C.lg));
+        const int in = (kvh << P.C.lg) + (pos & ((1 << P.C.lg) - 1));
         paged_append_row<KV>(P, theta, cc.b, kvh, pos, pid * P.C.page_stride + in,
-                             pid * ((int64_t)L.Hkv << P.C.lg) + in, stage);
+                             pid * (L.Hkv << P.C.lg) + in, stage);
       }
       paged_tile<KV>(A, stage, mask);
       __syncwarp();
-      if (i + NS < n) {
+      if (more) {
         tile_issue<KV>(P, nx, stage, masks + slot);
-        if (i + NS + 1 < n) {
+        more = pline < p1;
+        if (more) {
           nx = tile_desc(P, pc);
-          if (++pc.k == pc.nt) cursor_next_group(P, pc);
+          cursor_step(P, pc, pline);
         }
       }
       cp_async_commit();
@@ -996,7 +1016,8 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams P) {
       ++cc.k;
       ++line;
       const bool ends = cc.k == cc.nt;
-      if (ends || i == n - 1) {
+      const bool last = line + (ends ? kSetup : 0) >= p1;
+      if (ends || last) {
         attn_sum<KV>(A);
         const bool starts = seg_k == 0;
         if (starts && ends) {
@@ -1005,7 +1026,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams P) {
           // an open end: to the drained ring, or, where tiles of other groups follow and the ring
           // is in use, to the workspace for now (then it is of a group that an earlier warp began)
           float* dst = reinterpret_cast<float*>(ring) + (starts ? warp_part_floats(G) : 0);
-          if (i < n - 1) {
+          if (!last) {
             dst = P.head + (int64_t)(blockIdx.x * NW + warp) * warp_part_floats(G);
             has_head = true;
           } else {
@@ -1016,15 +1037,16 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams P) {
           if (lane == 0) {
             PagedEntry e;
             e.gid = cc.b * L.Hkv + cc.gi;
-            e.ge = line + (cc.nt - cc.k);
+            e.ge = ct0 + line + (cc.nt - cc.k);
             e.gs = e.ge - cc.nt;
             e.pad = 0;
             ent[2 * warp + (starts ? 1 : 0)] = e;
           }
         }
-        if (ends && i < n - 1) {
-          cursor_next_group(P, cc);
+        if (ends) {
           line += kSetup;
+          if (!last) cursor_next_group(P, cc);
+          fresh = true;
         }
       }
     }
@@ -1053,11 +1075,12 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams P) {
     const int before = __shfl_sync(0xffffffffu, gid, below ? 31 - __clz(below) : 0);
     const bool lead = gid >= 0 && (!below || before != gid);
     const uint32_t leads = __ballot_sync(0xffffffffu, lead);
-    const uint32_t left = __ballot_sync(0xffffffffu, lead && ent[lane & (2 * NW - 1)].gs < ct0);
-    const uint32_t right = __ballot_sync(0xffffffffu, lead && ent[lane & (2 * NW - 1)].ge > ct1) & ~left;
+    const PagedEntry* mine_e = ent + min(lane, 2 * NW - 1);
+    const uint32_t left = __ballot_sync(0xffffffffu, lead && mine_e->gs < ct0);
+    const uint32_t right = __ballot_sync(0xffffffffu, lead && mine_e->ge > ct1) & ~left;
     if (left) open_run[0] = __ffs(left) - 1;
     if (right) open_run[1] = __ffs(right) - 1;
-    int unit = 0;
+    int unit = 0;                                      // (at most 32 runs of 8 heads)
 #pragma unroll 1
     for (uint32_t todo = leads; todo; unit += G) {
       const int first = __ffs(todo) - 1;
@@ -1065,7 +1088,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams P) {
       todo &= todo - 1;
       if (todo) members &= (1u << (__ffs(todo) - 1)) - 1;
 #pragma unroll 1
-      for (int h = (warp - unit) & (NW - 1); h < G; h += NW) {
+      for (int h = (warp + 64 * NW - unit) % NW; h < G; h += NW) {
         float M = -INFINITY, MO = -INFINITY, Ls = 0.f;
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
@@ -1352,7 +1375,7 @@ paged_append_kernel(const __grid_constant__ PagedAppendParams P) {
     for (int e = 0; e < 8; ++e) k[e] = (float)kx[e];
     const int pid = slot >> P.C.lg;
     const int in = ((g0 + g) << P.C.lg) + (slot & ((1 << P.C.lg) - 1));
-    const int64_t row = pid * P.C.page_stride + in;
+    const int64_t row = pid * P.C.page_stride + in;    // below 2^31
     if (KV == kKvBf16) {
       // rounding twice differs from once only where single precision ends up in the middle of two
       // bf16 values (2^-16 of the elements), or has lost a small number's last places

@@ -124,7 +124,8 @@ BAD_CACHES = [
     (dict(page_size=8), "RTP_ESHAPE"), (dict(page_size=48), "RTP_ESHAPE"),
     (dict(page_size=512), "RTP_ESHAPE"), (dict(page_size=0), "RTP_ESHAPE"),
     (dict(n_pages=0), "RTP_ESHAPE"), (dict(n_pages=1 << 27), "RTP_ESHAPE"),
-    (dict(page_stride=127), "RTP_ESHAPE"),
+    (dict(page_stride=127), "RTP_ESHAPE"), (dict(page_stride=1 << 25), "RTP_ESHAPE"),
+    (dict(n_pages=1 << 24, page_size=64), "RTP_ESHAPE"),
 ]
 
 
