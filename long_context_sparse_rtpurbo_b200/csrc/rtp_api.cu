@@ -690,11 +690,12 @@ int rtp_paged_reserve(const rtp_page_pool* pool, const int32_t* lens, const int3
   P.lg = lg;
   P.status = static_cast<int*>(ws);
   P.arrive = at<uint32_t>(ws, 4 * kPagedReserveCounter);
-  // about two blocks of 32 pages a warp, as far as n_new tells, and at most one CTA per SM: one
-  // CTA for a decode step, which then needs no arrival
+  // A decode step of up to 512 sequences: one CTA, a thread each, no arrival (4.0 us against 6.4).
+  // Otherwise about two blocks of 32 pages a warp as far as n_new tells, or 32 sequences a CTA.
   const int64_t pages = n_new > 0 ? ((int64_t)n_new >> lg) + 2 : pool->table_stride;
-  const int64_t blocks = P.B * ((pages + 31) / 32);
-  const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(di.sms, blocks / (4 * kResWarps)));
+  int64_t ctas = P.B * ((pages + 31) / 32) / (2 * kResWarps);
+  if (n_new > 0 && n_new <= kResLittle) ctas = P.B <= kResThreads ? 1 : P.B / 32;
+  const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(di.sms, ctas));
   paged_reserve_kernel<<<grid, kResThreads, 8 * (size_t)P.B, (cudaStream_t)stream>>>(P);
   g_launches = 1;
   return cudaGetLastError() == cudaSuccess ? RTP_OK : RTP_ECUDA;

@@ -1447,24 +1447,62 @@ __device__ __forceinline__ int ring_place(int64_t x, int n) {
   return x >> 32 ? (int)(x % n) : (int)((uint32_t)x % (uint32_t)n);
 }
 
+constexpr int kResLittle = 4;                // tokens and page moves that one thread takes on
+
 // One sequence's wish: held and wanted pages. Invalid lengths hold and want nothing.
 struct ResWish { int n0, n1, h0, h1; bool bad; };
-__device__ __forceinline__ ResWish res_wish(const PagedReserveParams& P, int b) {
+__device__ __forceinline__ ResWish res_wish(const PagedReserveParams& P, int n0, int n1) {
   ResWish w;
-  w.n0 = P.lens[b];
-  w.n1 = P.new_lens[b];
+  w.n0 = n0;
+  w.n1 = n1;
   w.bad = w.n0 < 0 || w.n1 < 0 || w.n0 > P.cap || w.n1 > P.cap;
   const int64_t r = (1 << P.lg) - 1;
   w.h0 = w.bad ? 0 : (int)((w.n0 + r) >> P.lg);
   w.h1 = w.bad ? 0 : (int)((w.n1 + r) >> P.lg);
   return w;
 }
+// place i of the ring, i below twice its size
+__device__ __forceinline__ int64_t ring_at(const PagedReserveParams& P, int64_t i) {
+  return i >= P.n_pages ? i - P.n_pages : i;
+}
+// One thread's sequence: up to kResLittle page moves and slots. head, tail: its places in the ring.
+__device__ __forceinline__ void res_little(const PagedReserveParams& P, int b, int n0, int n1, bool granted,
+                                           int64_t head, int64_t tail) {
+  const ResWish x = res_wish(P, n0, n1);
+  int32_t* row = P.table + (int64_t)b * P.stride;
+  int id[kResLittle + 1];                    // the page of the first token, then those taken
+  const int pg0 = x.bad ? 0 : x.n0 >> P.lg;
+  id[0] = granted && pg0 < x.h0 && P.n_new > 0 ? row[pg0] : 0;
+#pragma unroll
+  for (int j = 0; j < kResLittle; ++j) {
+    if (granted && j < x.h1 - x.h0) {
+      id[j + 1] = P.free_pages[ring_at(P, head + j)];
+      row[x.h0 + j] = id[j + 1];
+    }
+    if (granted && j < x.h0 - x.h1) P.free_pages[ring_at(P, tail + j)] = row[x.h1 + j];
+  }
+#pragma unroll
+  for (int j = 0; j < kResLittle; ++j)
+    if (j < P.n_new) {
+      const int64_t pos = (int64_t)x.n0 + j;
+      int slot = -1;
+      if (granted && pos < x.n1) {
+        const int pg = (int)(pos >> P.lg);
+        int pid = id[0];                     // (pages are larger than kResLittle tokens: one or the next)
+        if (pg >= x.h0) pid = id[1];
+        slot = (pid << P.lg) + (int)(pos & ((1 << P.lg) - 1));
+      }
+      P.slot_map[(int64_t)b * P.n_new + j] = slot;
+    }
+}
 
 // Every CTA sums up the whole batch (its lengths come from L2): a thread takes up to 8
-// consecutive sequences, one scan over the block. Then the grid's warps share out the sequences,
-// W / B warps to one, 32 pages at a time: a lane per page loads its id (from the ring or the
-// table) once, writes the table entry, and the slots of those pages' tokens take the id by a
-// shuffle. Bound by the slot map's bytes for prompts, by the launch for a decode step.
+// consecutive sequences, one scan over the block. A sequence with little to do (a decode step's:
+// a few tokens and pages) is then done by the thread that summed it up. The others are shared out
+// among the grid's warps, W / B warps to one, 32 pages at a time: a lane per page loads its id
+// (from the ring or the table) once, writes the table entry, and the slots of those pages' tokens
+// take the id by a shuffle. Bound by the slot map's bytes for prompts, by the launch and the chain
+// of loads (lengths, counters, pages) for a decode step.
 // Nothing that a call reads is written before all CTAs have read it: the ring's taken and
 // returned entries are disjoint, held table entries are not rewritten, and the lengths and
 // counters are written by the CTA that arrives last, so they may be updated in place.
@@ -1475,21 +1513,25 @@ paged_reserve_kernel(const __grid_constant__ PagedReserveParams P) {
   uint32_t* back = rsm + P.B;                // [B] pages returned before each sequence
   __shared__ uint32_t wsum[2][kResWarps];
   __shared__ uint32_t s_taken, s_bad, s_last;
+  __shared__ int s_hm, s_tm;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) { s_taken = 0; s_bad = 0; }
   const int64_t head = P.counters[0], tail = P.counters[1];
   const int per = (P.B + kResThreads - 1) / kResThreads, first = tid * per;
+  int n0[kResPer], n1[kResPer];
   uint32_t need[kResPer], ret[kResPer], a = 0, c = 0;
   bool bad = false;
 #pragma unroll
   for (int k = 0; k < kResPer; ++k) {
-    need[k] = ret[k] = 0;
-    if (k < per && first + k < P.B) {
-      const ResWish w = res_wish(P, first + k);
-      need[k] = max(w.h1 - w.h0, 0);
-      ret[k] = max(w.h0 - w.h1, 0);
-      bad = bad || w.bad;
-    }
+    n0[k] = n1[k] = 0;
+    if (k < per && first + k < P.B) { n0[k] = P.lens[first + k]; n1[k] = P.new_lens[first + k]; }
+  }
+#pragma unroll
+  for (int k = 0; k < kResPer; ++k) {
+    const ResWish w = res_wish(P, n0[k], n1[k]);
+    need[k] = max(w.h1 - w.h0, 0);
+    ret[k] = max(w.h0 - w.h1, 0);
+    bad = bad || w.bad;
     a = add_sat(a, need[k]);
     c = add_sat(c, ret[k]);
   }
@@ -1503,6 +1545,10 @@ paged_reserve_kernel(const __grid_constant__ PagedReserveParams P) {
   // exclusive: the neighbour's inclusive sum (a saturated one cannot be taken apart)
   uint32_t ea = __shfl_up_sync(0xffffffffu, ia, 1), ec = __shfl_up_sync(0xffffffffu, ic, 1);
   if (lane == 0) ea = ec = 0;
+  const bool sane = head >= 0 && tail >= head && tail - head <= P.n_pages;
+  const uint32_t avail = sane ? (uint32_t)(tail - head) : 0;
+  if (warp == kResWarps - 1 && lane < 2)     // the warp with least to do
+    (lane ? s_tm : s_hm) = sane ? ring_place(lane ? tail : head, P.n_pages) : 0;
   __syncthreads();
   uint32_t run_c;                            // all returned pages
   {
@@ -1517,83 +1563,94 @@ paged_reserve_kernel(const __grid_constant__ PagedReserveParams P) {
     const uint32_t bc = __shfl_sync(0xffffffffu, vc, max(warp - 1, 0));
     if (warp > 0) { ea = add_sat(ea, ba); ec = add_sat(ec, bc); }
   }
-  const bool sane = head >= 0 && tail >= head && tail - head <= P.n_pages;
-  const uint32_t avail = sane ? (uint32_t)(tail - head) : 0;
-  uint32_t taken = 0;
+  // more pages than the ring has room for: the lengths or counters are not this pool's
+  const bool ok = sane && (int64_t)avail + run_c <= P.n_pages;
+  const int hm = s_hm, tm = s_tm;
+  const bool few = P.n_new <= kResLittle;
+  uint32_t taken = 0, served = 0;            // served: bit k of this thread's sequences
+  bool heavy = false;                        // some are left to the warps
 #pragma unroll
   for (int k = 0; k < kResPer; ++k) {
     if (k < per && first + k < P.B) {
-      upto[first + k] = ea;
-      back[first + k] = ec;
+      const int b = first + k;
+      const bool granted = ok && !res_wish(P, n0[k], n1[k]).bad && (need[k] == 0 || add_sat(ea, need[k]) <= avail);
+      served |= (uint32_t)granted << k;
+      upto[b] = ea;
+      back[b] = ec;
+      if (need[k] && granted) taken = ea + need[k];
+      if (few && need[k] <= kResLittle && ret[k] <= kResLittle) {
+        if (blockIdx.x == b % gridDim.x) res_little(P, b, n0[k], n1[k], granted, hm + ea, tm + ec);
+      } else {
+        heavy = true;
+      }
     }
     ea = add_sat(ea, need[k]);
     ec = add_sat(ec, ret[k]);
-    if (need[k] && ea <= avail) taken = ea;
   }
   taken = __reduce_max_sync(0xffffffffu, taken);
   if (lane == 0 && taken) atomicMax(&s_taken, taken);
   if (bad) s_bad = 1;
-  __syncthreads();
-  // more pages than the ring has room for: the lengths or counters are not this pool's
-  const bool ok = sane && (int64_t)avail + run_c <= P.n_pages;
+  const bool work = __syncthreads_or(heavy);
   if (tid == 0 && blockIdx.x == 0 && (!ok || s_bad)) set_status(P.status, -6);
-  const int hm = ok ? ring_place(head, P.n_pages) : 0, tm = ok ? ring_place(tail, P.n_pages) : 0;
 
-  const int W = gridDim.x * kResWarps, share = max(1, W / P.B);     // warps of a sequence
-  const int w = blockIdx.x * kResWarps + warp, teams = W / share;
-  for (int b = w / share; b < P.B && w < teams * share; b += teams) {
-    const ResWish x = res_wish(P, b);
-    const int64_t u0 = upto[b], r0 = back[b];
-    const bool granted = ok && !x.bad && (x.h1 <= x.h0 || u0 + (x.h1 - x.h0) <= avail);
-    const int n1 = granted ? x.n1 : x.n0, h1 = granted ? x.h1 : x.h0;
-    int32_t* row = P.table + (int64_t)b * P.stride;
-    int32_t* slots = P.slot_map + (int64_t)b * P.n_new;
-    // pages returned
-    for (int j = (w % share) * 32 + lane; j < x.h0 - h1; j += 32 * share) {
-      int64_t at = tm + r0 + j;
-      if (at >= P.n_pages) at -= P.n_pages;
-      P.free_pages[at] = row[h1 + j];
-    }
-    // pages from the one that the first new token goes to, 32 at a time; then the places of
-    // slot_map behind the last page
-    const int pg0 = x.bad ? 0 : x.n0 >> P.lg;
-    const int chunks = max(h1 - pg0, 0) + 31 >> 5;
-    for (int ch = w % share; ch < chunks; ch += share) {
-      const int pg = pg0 + 32 * ch + lane;
-      int id = 0;
-      if (pg < x.h0) {
-        id = row[pg];
-      } else if (pg < h1) {
-        int64_t at = hm + u0 + (pg - x.h0);
-        if (at >= P.n_pages) at -= P.n_pages;
-        id = P.free_pages[at];
-        row[pg] = id;
+  if (work) {
+    const int W = gridDim.x * kResWarps, share = max(1, W / P.B);     // warps of a sequence
+    const int w = blockIdx.x * kResWarps + warp, teams = W / share;
+    // a lane loads the lengths of one of this warp's next 32 sequences
+    int la = 0, lb = 0, i = 0;
+#pragma unroll 1
+    for (int b = w / share; b < P.B && w < teams * share; b += teams, ++i) {
+      if ((i & 31) == 0 && b + lane * (int64_t)teams < P.B) {
+        la = P.lens[b + lane * teams];
+        lb = P.new_lens[b + lane * teams];
       }
-      // tokens of these pages: positions from p0, at least n0
-      const int64_t p0 = (int64_t)(pg0 + 32 * ch) << P.lg;
-      const int64_t end = min(min(p0 + (32 << P.lg), (int64_t)n1), (int64_t)x.n0 + P.n_new);
-      const int64_t start = max(p0, (int64_t)x.n0);
+      const ResWish x = res_wish(P, __shfl_sync(0xffffffffu, la, i & 31), __shfl_sync(0xffffffffu, lb, i & 31));
+      if (few && abs(x.h1 - x.h0) <= kResLittle) continue;
+      const int64_t u0 = upto[b], r0 = back[b];
+      const bool granted = ok && !x.bad && (x.h1 <= x.h0 || u0 + (x.h1 - x.h0) <= avail);
+      const int n1 = granted ? x.n1 : x.n0, h1 = granted ? x.h1 : x.h0;
+      int32_t* row = P.table + (int64_t)b * P.stride;
+      int32_t* slots = P.slot_map + (int64_t)b * P.n_new;
+      // pages returned
+      for (int j = (w % share) * 32 + lane; j < x.h0 - h1; j += 32 * share)
+        P.free_pages[ring_at(P, tm + r0 + j)] = row[h1 + j];
+      // pages from the one that the first new token goes to, 32 at a time; then the places of
+      // slot_map behind the last page
+      const int pg0 = x.bad ? 0 : x.n0 >> P.lg;
+      const int chunks = (max(h1 - pg0, 0) + 31) >> 5;
+      for (int ch = w % share; ch < chunks; ch += share) {
+        const int pg = pg0 + 32 * ch + lane;
+        int id = 0;
+        if (pg < x.h0) {
+          id = row[pg];
+        } else if (pg < h1) {
+          id = P.free_pages[ring_at(P, hm + u0 + (pg - x.h0))];
+          row[pg] = id;
+        }
+        // tokens of these pages: positions from p0, at least n0
+        const int64_t p0 = (int64_t)(pg0 + 32 * ch) << P.lg;
+        const int64_t end = min(min(p0 + (32 << P.lg), (int64_t)n1), (int64_t)x.n0 + P.n_new);
+        const int64_t start = max(p0, (int64_t)x.n0);
 #pragma unroll 4
-      for (int64_t p = start; p < end; p += 32) {
-        const int64_t pos = p + lane;
-        const int pid = __shfl_sync(0xffffffffu, id, (int)(min(pos, end - 1) - p0) >> P.lg);
-        if (pos < end) slots[pos - x.n0] = (pid << P.lg) + (int)(pos & ((1 << P.lg) - 1));
+        for (int64_t p = start; p < end; p += 32) {
+          const int64_t pos = p + lane;
+          const int pid = __shfl_sync(0xffffffffu, id, (int)(min(pos, end - 1) - p0) >> P.lg);
+          if (pos < end) slots[pos - x.n0] = (pid << P.lg) + (int)(pos & ((1 << P.lg) - 1));
+        }
       }
+      const int got = min(max(n1 - x.n0, 0), P.n_new);
+      for (int j = (x.bad ? 0 : got) + (w % share) * 32 + lane; j < P.n_new; j += 32 * share)
+        slots[j] = -1;
     }
-    const int got = min(max(n1 - x.n0, 0), P.n_new);
-    for (int j = (x.bad ? 0 : got) + (w % share) * 32 + lane; j < P.n_new; j += 32 * share)
-      slots[j] = -1;
   }
   // lengths and counters, once every CTA has read them
   __syncthreads();
   if (tid == 0) s_last = gridDim.x == 1 || atomicInc(P.arrive, gridDim.x - 1) == gridDim.x - 1;
   __syncthreads();
   if (!s_last) return;
-  for (int b = tid; b < P.B; b += kResThreads) {
-    const ResWish x = res_wish(P, b);
-    const bool granted = ok && !x.bad && (x.h1 <= x.h0 || (int64_t)upto[b] + (x.h1 - x.h0) <= avail);
-    P.lens_out[b] = granted ? x.n1 : x.n0;
-  }
+#pragma unroll
+  for (int k = 0; k < kResPer; ++k)
+    if (k < per && first + k < P.B) P.lens_out[first + k] = (served >> k) & 1u ? n1[k] : n0[k];
   if (tid == 0) {
     P.counters_out[0] = ok ? head + s_taken : head;
     P.counters_out[1] = ok ? tail + run_c : tail;
