@@ -639,7 +639,8 @@ int paged_decode_impl(const rtp_layer_desc* desc, const rtp_paged_cache* cache,
   P.status = static_cast<int*>(ws);
   P.arrive = at<uint32_t>(ws, 256);
   P.part = at<float>(ws, kPagedCtrlBytes);
-  P.head = P.part + (size_t)2 * kPagedMaxCTAs * cta_part_floats(P.L.G);
+  P.head = P.part + (size_t)2 * kPagedMaxRanges * cta_part_floats(P.L.G);
+  P.queue = at<uint32_t>(ws, 4 * kPagedQueue);
   cudaStream_t st = (cudaStream_t)stream;
   if (cache->kv_type == RTP_KV_BF16)
     return append ? launch_paged<kKvBf16, true>(P, di, st) : launch_paged<kKvBf16, false>(P, di, st);

@@ -23,8 +23,11 @@ namespace rtp {
 
 constexpr int kKvBf16 = 0, kKvE4m3 = 1;
 constexpr int kPagedMaxCTAs = 160;
+constexpr int kPagedMaxRanges = 2 * kPagedMaxCTAs;
+constexpr int kLaterShare = 8;              // 1 / this of a long line is left to the CTAs done first
 constexpr int kPagedCtrlBytes = 4096;       // status word at 0, arrival counters from 256
 constexpr int kPagedReserveCounter = 960;   // word index of the reservation's arrival counter
+constexpr int kPagedQueue = 961;            // word index of the decode step's queue of later ranges
 constexpr float kE4m3Max = 448.f;
 constexpr float kScaleMin = 1.17549435e-38f;   // 2^-126
 
@@ -44,18 +47,20 @@ struct PagedDecodeParams {
   uint16_t* out;
   float* lse;
   int* status;
-  uint32_t* arrive;
-  float *part, *head;            // [CTAs][2] partials of CTAs, [CTAs][16] of warps
+  uint32_t *arrive, *queue;
+  float *part, *head;            // [ranges][2] partials of ranges, [CTAs][16] of warps
 };
 
 template <int KV> struct PagedCfg;
 template <> struct PagedCfg<kKvBf16> {
   static constexpr int kWarps = 8, kStages = 3, kRowB = 256, kTerms = 3;
   static constexpr int kStageB = 16 * 512;
+  static constexpr bool kLater = true;         // ranges for the CTAs done first
 };
 template <> struct PagedCfg<kKvE4m3> {
   static constexpr int kWarps = 12, kStages = 4, kRowB = 128, kTerms = 2;
   static constexpr int kStageB = 16 * 256 + 128;
+  static constexpr bool kLater = false;
 };
 
 
@@ -69,7 +74,7 @@ constexpr int kPartPitch = 132;
 __host__ __device__ constexpr int warp_part_floats(int G) { return G * kPartPitch + 32; }
 __host__ __device__ constexpr int cta_part_floats(int G) { return G * kD + 32; }
 __host__ __device__ constexpr size_t paged_part_floats(int G) {
-  return (size_t)2 * kPagedMaxCTAs * cta_part_floats(G) +
+  return (size_t)2 * kPagedMaxRanges * cta_part_floats(G) +
          (size_t)kPagedMaxCTAs * kPagedMaxWarps * warp_part_floats(G);
 }
 
@@ -79,6 +84,8 @@ struct PagedEntry {              // an open end of a warp's range
   int pad;
 };
 
+// Places a warp from which on a share of the line is left to the CTAs done first
+constexpr int kLaterPlaces = 128;
 // Tiles per warp up to which a group stays in one CTA, where every group can have one
 constexpr int kOneCta = 5;
 
@@ -94,8 +101,8 @@ struct PagedSmem {
   static constexpr int kEnt = kMask + Cfg::kWarps * 8 * 4;
   static constexpr int kPrefix = kEnt + kEntries * (int)sizeof(PagedEntry);   // [129]
   static constexpr int kMisc = kPrefix + 130 * 8;
-  static constexpr int kWt = kMisc + 256;                          // [160][8] weights of a merge
-  static constexpr int kBytes = kWt + kPagedMaxCTAs * 8 * 4;
+  static constexpr int kWt = kMisc + 256;                          // [ranges][8] weights of a merge
+  static constexpr int kBytes = kWt + (Cfg::kLater ? kPagedMaxRanges : kPagedMaxCTAs) * 8 * 4;
   static_assert(2 * warp_part_floats(8) * 4 <= Cfg::kStages * Cfg::kStageB, "a drained ring holds two partials");
 };
 
@@ -295,31 +302,44 @@ __device__ __forceinline__ I warp_incl_sum(I x) {
   return x;
 }
 
-// The line cut into n <= 160 ranges, the first `extra` of them one place longer. Plain 64-bit
-// divisions cost about 500 cycles each here; there is one left, for lines beyond 2^32 places.
+// The line cut into ranges: n equal ones, one for each CTA (the first `extra` of them a place
+// longer), and behind place T1 n2 smaller ones, which the CTAs that are done first take.
+// Plain 64-bit divisions cost about 500 cycles each here; one is left, for lines beyond 2^32.
 struct LineSplit {
-  long long each;
-  int n, extra;
+  long long each, T1;
+  int n, extra, n2, each2, extra2;
 };
-__device__ __forceinline__ LineSplit split_line(long long T, int n) {
+template <bool LATER>
+__device__ __forceinline__ LineSplit split_line(long long T, int n, int n2) {
+  if (!LATER) n2 = 0;
   LineSplit s;
   s.n = n;
-  s.each = T >> 32 ? T / n : (long long)((uint32_t)T / (uint32_t)n);
-  s.extra = (int)(T - s.each * n);
+  s.n2 = n2;
+  s.T1 = n2 ? T - T / kLaterShare : T;
+  s.each = s.T1 >> 32 ? s.T1 / n : (long long)((uint32_t)s.T1 / (uint32_t)n);
+  s.extra = (int)(s.T1 - s.each * n);
+  s.each2 = n2 ? (int)((T - s.T1) / n2) : 0;
+  s.extra2 = n2 ? (int)(T - s.T1 - (long long)s.each2 * n2) : 0;
   return s;
 }
+template <bool LATER>
 __device__ __forceinline__ long long range_start(const LineSplit& s, int i) {
-  return s.each * i + min(i, s.extra);
+  if (!LATER || i < s.n) return s.each * i + min(i, s.extra);
+  i -= s.n;
+  return s.T1 + (long long)s.each2 * i + min(i, s.extra2);
 }
-// The range that holds a place: the quotient is below 160, so its single-precision estimate is
+// The range that holds a place: a quotient is at most 160, so its single-precision estimate is
 // off by one at most.
+template <bool LATER>
 __device__ __forceinline__ int range_of(const LineSplit& s, long long place) {
-  int i = min((int)__fdividef((float)place, (float)(s.each + 1)), s.n - 1);
-  if (i >= s.extra)
-    i = min(s.extra + (int)__fdividef((float)(place - s.extra * (s.each + 1)), (float)s.each), s.n - 1);
-  if (range_start(s, i) > place) --i;
-  if (i + 1 < s.n && range_start(s, i + 1) <= place) ++i;
-  return i;
+  const bool later = LATER && place >= s.T1;
+  const long long x = later ? place - s.T1 : place, each = later ? s.each2 : s.each;
+  const int extra = later ? s.extra2 : s.extra, n = later ? s.n2 : s.n;
+  int i = min((int)__fdividef((float)x, (float)(each + 1)), n - 1);
+  if (i >= extra) i = min(extra + (int)__fdividef((float)(x - extra * (each + 1)), (float)each), n - 1);
+  if (each * i + min(i, extra) > x) --i;
+  if (i + 1 < n && each * (i + 1) + min(i + 1, extra) <= x) ++i;
+  return later ? s.n + i : i;
 }
 
 struct TileDesc { int pid, row; uint32_t mask; };   // page, row in the page block, rows attended
@@ -888,6 +908,8 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams P) {
   // ---- this CTA's range
   long long ct0, ct1;
   LineSplit split;
+  int* next_range = reinterpret_cast<int*>(sm + S::kMisc + 112);
+  int range = blockIdx.x, later = 0;                   // later: ranges that are left to whoever is first
   {
     const uint32_t live = __ballot_sync(0xffffffffu, lens > 0);
     const int x = nc > 1 ? 0 : __reduce_max_sync(0xffffffffu, L.n_ret ? (lens + 15) >> 4 : local_tiles(L, lens).nt);
@@ -911,12 +933,25 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams P) {
       if (T < (long long)ctas * NW) ctas = ((int)T + NW - 1) / NW;
       if (nc == 1 && T < (1 << 20))
         ctas = min(ctas, (int)(sqrtf(64.f / (NW * G) / (float)x) * (float)T) + 1);
-      split = split_line(T, ctas);
+      // The SMs get unequal shares of the bandwidth (15 % more and less than the median). On a long
+      // line the CTAs that are done first take what was left for that, range by range: 4 % with
+      // bf16 rows. (Not with e4m3 rows, whose SMs are busy computing and more even; and a line
+      // of 57 places a warp lost 6 % to the joins of the additional ranges.)
+      if (Cfg::kLater && ctas == gridDim.x && T >= (long long)ctas * NW * kLaterPlaces) later = ctas;
+      split = split_line<Cfg::kLater>(T, ctas, later);
       if (blockIdx.x >= split.n) return;
-      ct0 = range_start(split, blockIdx.x);
-      ct1 = range_start(split, blockIdx.x + 1);
+      ct0 = range_start<Cfg::kLater>(split, blockIdx.x);
+      ct1 = range_start<Cfg::kLater>(split, blockIdx.x + 1);
     }
   }
+  unsigned char* ring = sm + warp * NS * Cfg::kStageB;
+  const uint32_t ring_s = smem_u32(ring);
+  auto entry_part = [&](int j) {
+    return reinterpret_cast<const float*>(sm + (j >> 1) * NS * Cfg::kStageB) + (j & 1) * warp_part_floats(G);
+  };
+
+#pragma unroll 1
+  while (true) {
   const int len = (int)(ct1 - ct0);                    // below 2^31: a sequence has 2^26 places at most
   // this warp's places, counted from ct0
   int line = (int)((long long)warp * len / NW);        // place of the tile at cc
@@ -929,6 +964,8 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams P) {
       for (int i = lane; i < nc; i += 32) before += prefix[i] <= p0;
       chunk = __reduce_add_sync(0xffffffffu, before) - 1;
       base = prefix[chunk];
+    }
+    if (nc > 1 || (Cfg::kLater && range != blockIdx.x)) {
       lens = paged_len(P, chunk * 32 + lane, nullptr);
       mine = seq_places(L, lens);
       incl = warp_incl_sum(mine);
@@ -939,8 +976,6 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams P) {
   }
   __syncthreads();                                     // theta, ent
 
-  unsigned char* ring = sm + warp * NS * Cfg::kStageB;
-  const uint32_t ring_s = smem_u32(ring);
   PagedAttn<KV> A;
   if (line < p1) {
     Cursor pc = cc;
@@ -1061,9 +1096,6 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams P) {
     }
   }
   __syncthreads();
-  auto entry_part = [&](int j) {
-    return reinterpret_cast<const float*>(sm + (j >> 1) * NS * Cfg::kStageB) + (j & 1) * warp_part_floats(G);
-  };
 
   // ---- the open ends of this CTA's warps: the entries of a group (a run) are merged in the order
   // of the line, one (run, head) a warp. (The code is kept small: it runs once, and most of its
@@ -1117,23 +1149,23 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams P) {
           *reinterpret_cast<uint2*>(P.out + head * kD + 4 * lane) = w;
           if (P.lse && lane == 0) P.lse[head] = (M + log2f(Ls)) * 0.6931471805599453f;
         } else {
-          float* gp = P.part + (int64_t)(blockIdx.x * 2 + (first == open_run[0] ? 0 : 1)) * cta_part_floats(G);
+          float* gp = P.part + (int64_t)((Cfg::kLater ? range : (int)blockIdx.x) * 2 + (first == open_run[0] ? 0 : 1)) * cta_part_floats(G);
           *reinterpret_cast<float4*>(gp + h * kD + 4 * lane) = s;
           if (lane < 3) gp[G * kD + 3 * h + lane] = lane == 0 ? M : lane == 1 ? Ls : MO;
         }
       }
     }
   }
-  if (open_run[0] < 0 && open_run[1] < 0) return;
+  if (open_run[0] >= 0 || open_run[1] >= 0) {
   __syncthreads();
-  // a group that spans CTAs c0..c1 counts its arrivals at c0's word, which wraps to zero
+  // a group that spans ranges c0..c1 counts its arrivals at c0's word, which wraps to zero
   int* finish = reinterpret_cast<int*>(sm + S::kMisc);
   if (tid < 2) {
     const int first = tid ? open_run[1] : open_run[0];
     int last = 0;
     if (first >= 0) {
       const PagedEntry e = ent[first];
-      const int c0 = range_of(split, e.gs), c1 = range_of(split, e.ge - 1);
+      const int c0 = range_of<Cfg::kLater>(split, e.gs), c1 = range_of<Cfg::kLater>(split, e.ge - 1);
       // the CTA's partial before the arrival, the others' after it
       uint32_t old;
       asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;"
@@ -1152,8 +1184,8 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams P) {
   for (int x = 0; x < 2; ++x) {
     if (!finish[x]) continue;
     const PagedEntry e = ent[x ? open_run[1] : open_run[0]];
-    const int c0 = range_of(split, e.gs), np = range_of(split, e.ge - 1) - c0 + 1;
-    // part i: the open end of CTA c0 + i (its last group for i = 0, its first otherwise)
+    const int c0 = range_of<Cfg::kLater>(split, e.gs), np = range_of<Cfg::kLater>(split, e.ge - 1) - c0 + 1;
+    // part i: the open end of range c0 + i (its last group for i = 0, its first otherwise)
     const float* part = P.part + (int64_t)c0 * 2 * pf;
     const int b = small_div(e.gid, L.Hkv);
     const int64_t head0 = (int64_t)b * L.Hq + (int64_t)kv_head(L, e.gid - b * L.Hkv) * G;
@@ -1171,31 +1203,45 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams P) {
     };
     copy(0, min(np, fit));
     if (warp < G) {
-      float m[kPagedMaxCTAs / 32], l[kPagedMaxCTAs / 32], mo[kPagedMaxCTAs / 32];
+      // up to 160 parts (all, but for one group over a long line) from registers
+      constexpr int kHeld = kPagedMaxCTAs / 32;
+      float m[kHeld], l[kHeld], mo[kHeld];
       float M = -INFINITY, MO = -INFINITY, Ls = 0.f;
+      auto state = [&](int i) { return part + (i * 2 + (i == 0)) * pf + G * kD + 3 * warp; };
 #pragma unroll
-      for (int u = 0; u < kPagedMaxCTAs / 32; ++u) {
+      for (int u = 0; u < kHeld; ++u) {
         const int i = lane + 32 * u;
-        const float* q = part + (i * 2 + (i == 0)) * pf + G * kD + 3 * warp;
-        m[u] = i < np ? __ldcg(q) : -INFINITY;
-        l[u] = i < np ? __ldcg(q + 1) : 0.f;
-        mo[u] = i < np ? __ldcg(q + 2) : -INFINITY;
+        m[u] = i < np ? __ldcg(state(i)) : -INFINITY;
+        l[u] = i < np ? __ldcg(state(i) + 1) : 0.f;
+        mo[u] = i < np ? __ldcg(state(i) + 2) : -INFINITY;
       }
 #pragma unroll
-      for (int u = 0; u < kPagedMaxCTAs / 32; ++u) { M = fmaxf(M, m[u]); MO = fmaxf(MO, mo[u]); }
+      for (int u = 0; u < kHeld; ++u) { M = fmaxf(M, m[u]); MO = fmaxf(MO, mo[u]); }
+      if (Cfg::kLater)
+#pragma unroll 1
+        for (int i = lane + 32 * kHeld; i < np; i += 32) {
+          M = fmaxf(M, __ldcg(state(i)));
+          MO = fmaxf(MO, __ldcg(state(i) + 2));
+        }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
         M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
         MO = fmaxf(MO, __shfl_xor_sync(0xffffffffu, MO, o));
       }
 #pragma unroll
-      for (int u = 0; u < kPagedMaxCTAs / 32; ++u) {
+      for (int u = 0; u < kHeld; ++u) {
         const int i = lane + 32 * u;
         if (i < np) {
           Ls += l[u] * ex2_from(m[u], M);
           wt[i * 8 + warp] = ex2_from(mo[u], MO);
         }
       }
+      if (Cfg::kLater)
+#pragma unroll 1
+        for (int i = lane + 32 * kHeld; i < np; i += 32) {
+          Ls += __ldcg(state(i) + 1) * ex2_from(__ldcg(state(i)), M);
+          wt[i * 8 + warp] = ex2_from(__ldcg(state(i) + 2), MO);
+        }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) Ls += __shfl_xor_sync(0xffffffffu, Ls, o);
       if (lane == 0) {
@@ -1238,6 +1284,22 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams P) {
       *reinterpret_cast<uint2*>(P.out + head0 * kD + 4 * it) = w;
     }
     __syncthreads();
+  }
+  }
+  if (!Cfg::kLater || later == 0) return;
+  // ---- the next range that nobody has taken; each CTA comes here once too often, so the count
+  // wraps to zero
+  __syncthreads();                                     // the rings and entries are free
+  if (tid == 0) {
+    const uint32_t old = atomicInc(P.queue, (uint32_t)(split.n + later - 1));
+    *next_range = old < (uint32_t)later ? split.n + (int)old : -1;
+  }
+  if (tid < 2 * NW) ent[tid].gid = -1;
+  __syncthreads();
+  range = *next_range;
+  if (range < 0) return;
+  ct0 = range_start<Cfg::kLater>(split, range);
+  ct1 = range_start<Cfg::kLater>(split, range + 1);
   }
 }
 
