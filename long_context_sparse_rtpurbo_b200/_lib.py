@@ -61,6 +61,24 @@ class RtpPagePool(ctypes.Structure):
 
 
 _lib = None
+_native = None
+
+
+def native():
+    """The native binding of the paged calls, bound to the loaded librtp.so; raises if it has not been
+    built."""
+    global _native
+    if _native is None:
+        lib = load()
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise RuntimeError("_binding.so is not built; run __graft_entry__.build() first") from e
+        _binding.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            lib.rtp_paged_reserve, lib.rtp_paged_append_kv, lib.rtp_paged_decode_step,
+            lib.rtp_paged_decode_step_append)))
+        _native = _binding
+    return _native
 
 
 def load(path: str = LIB_PATH) -> ctypes.CDLL:

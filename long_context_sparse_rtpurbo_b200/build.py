@@ -1,8 +1,10 @@
-"""Builds librtp.so (sm_100a) in-tree with nvcc."""
+"""Builds librtp.so (sm_100a) in-tree with nvcc, and the native Python binding of its paged calls
+(_binding.so) with g++."""
 from __future__ import annotations
 
 import os
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
@@ -35,5 +37,24 @@ def build_checks(verbose: bool = False) -> str:
     return build(verbose, ["-DRTP_CHECKS"], "librtp_checks.so")
 
 
+def build_binding(verbose: bool = False) -> str:
+    """_binding.so: Python calls of the paged entry points (csrc/binding.cpp). It calls librtp.so by
+    address and links only against the PyTorch that is installed."""
+    import torch
+    from torch.utils import cpp_extension as ext
+    out = os.path.join(HERE, "_binding.so")
+    inc = [sysconfig.get_paths()["include"], "/usr/local/cuda/include", *ext.include_paths()]
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[f"-I{d}" for d in inc], os.path.join(HERE, "csrc", "binding.cpp"), "-o", out,
+           f"-L{lib}", f"-Wl,-rpath,{lib}", "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd))
+    subprocess.run(cmd, check=True)
+    return out
+
+
 if __name__ == "__main__":
+    print(build_binding(verbose=True))
     print(build(verbose=True))

@@ -67,6 +67,7 @@ class LayerDesc:
         self.c = RtpLayerDesc(B, Hq, Hkv, head_dim, idx_dim, sinks, window, 0, float(rope_base),
                               int(max_seq_len),
                               self.slots.ctypes.data_as(ctypes.POINTER(ctypes.c_int32)))
+        self.addr = ctypes.addressof(self.c)
         self.n_ret = int((self.slots >= 0).sum())
         self.n_loc = int((self.slots < 0).sum())
 
@@ -145,8 +146,9 @@ def rtp_prefill(desc: LayerDesc, q_pre, k_pre, v, n_b, n_max, out, ws=None, ws_b
 
 
 # ------------------------------------------------------------------------------- paged caches
-# The calls below check dtype, size, contiguity and device of every tensor: a paged call is cheap
-# enough to be made with the wrong one of many buffers. All tensors must be on the current device.
+# The calls below check type, size, contiguity and device of every tensor (csrc/binding.cpp): a
+# paged call is cheap enough to be made with the wrong one of many buffers. All tensors must be on
+# the current device.
 
 def _arg(t: torch.Tensor, what: str, dtype, n: int, dev: int, optional=False) -> int | None:
     if t is None and optional:
@@ -157,20 +159,8 @@ def _arg(t: torch.Tensor, what: str, dtype, n: int, dev: int, optional=False) ->
     return t.data_ptr()
 
 
-def _ws_arg(ws: torch.Tensor, dev: int) -> tuple[int | None, int]:
-    if ws is None:
-        return None, 0
-    if ws.get_device() != dev or not ws.is_contiguous():
-        raise ValueError(f"workspace: a contiguous tensor on cuda:{dev} is wanted")
-    return ws.data_ptr(), ws.numel() * ws.element_size()
-
-
-def _stream_on(stream, dev: int) -> int:
-    if torch.cuda.current_device() != dev:
-        raise ValueError(f"tensors are on cuda:{dev}, which is not the current device")
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+def _stream_arg(stream) -> int | None:
+    return stream if stream is None else getattr(stream, "cuda_stream", stream)
 
 
 class PagedCache:
@@ -205,7 +195,7 @@ class PagedCache:
             _arg(v_scale, "v_scale", torch.float32, n, dev, True),
             k.stride(0) // 128 if n_pages > 1 else 0,
             _arg(block_table, "block_table", torch.int32, self.B * self.table_stride, dev))
-        self.ref = ctypes.byref(self.c)
+        self.addr = ctypes.addressof(self.c)
 
 
 def make_paged_cache(k, v, block_table, k_scale=None, v_scale=None) -> PagedCache:
@@ -229,7 +219,7 @@ class PagePoolRef:
             self.B, int(page_size), self.n_pages, self.table_stride,
             _arg(free_pages, "free_pages", torch.int32, self.n_pages, dev),
             _arg(block_table, "block_table", torch.int32, self.B * self.table_stride, dev))
-        self.ref = ctypes.byref(self.c)
+        self.addr = ctypes.addressof(self.c)
 
 
 def make_page_pool(free_pages, block_table, page_size) -> PagePoolRef:
@@ -251,68 +241,50 @@ def rtp_paged_reserve(pool: PagePoolRef, lens, new_lens, counters, lens_out, cou
                       n_new, ws, stream=None):
     """Block tables and slot maps for new lengths (see include/rtp.h). lens, new_lens, lens_out:
     int32 [B]; counters, counters_out: int64 [2]; slot_map: int32 [B][n_new]."""
-    B, dev = pool.B, pool.device_index
-    w, wb = _ws_arg(ws, dev)
-    return _check("rtp_paged_reserve", _lib.load().rtp_paged_reserve(
-        pool.ref, _arg(lens, "lens", torch.int32, B, dev),
-        _arg(new_lens, "new_lens", torch.int32, B, dev),
-        _arg(counters, "counters", torch.int64, 2, dev),
-        _arg(lens_out, "lens_out", torch.int32, B, dev),
-        _arg(counters_out, "counters_out", torch.int64, 2, dev),
-        _arg(slot_map, "slot_map", torch.int32, B * n_new, dev, n_new == 0), n_new, w, wb,
-        _stream_on(stream, dev)))
+    return _check("rtp_paged_reserve", (_lib._native or _lib.native()).reserve(
+        pool.addr, pool.B, pool.device_index, lens, new_lens, counters, lens_out, counters_out,
+        slot_map, n_new, ws, _stream_arg(stream)))
+
+
+def _paged_fits(desc: LayerDesc, cache: PagedCache):
+    """The description's struct, if it goes with the cache."""
+    c = desc.c
+    if cache.Hkv != c.Hkv or cache.B != c.B:
+        raise ValueError(f"a cache of {cache.Hkv} KV heads and {cache.B} sequences does not go with "
+                         f"a description of {c.Hkv} and {c.B}")
+    return c
 
 
 def rtp_paged_append_kv(desc: LayerDesc, cache: PagedCache, k_pre, v, start_pos, slot_map, n_new,
                         ws=None, stream=None):
     """New tokens to their slots (see include/rtp.h). k_pre, v: bf16 [B][n_new][Hkv][128];
     start_pos: int32 [B]; slot_map: int32 [B][n_new]."""
-    B, dev = desc.c.B, cache.device_index
     _paged_fits(desc, cache)
-    n = B * n_new * cache.Hkv * 128
-    return _check("rtp_paged_append_kv", _lib.load().rtp_paged_append_kv(
-        desc.ref, cache.ref, _arg(k_pre, "k_pre", torch.bfloat16, n, dev),
-        _arg(v, "v", torch.bfloat16, n, dev), _arg(start_pos, "start_pos", torch.int32, B, dev),
-        _arg(slot_map, "slot_map", torch.int32, B * n_new, dev), n_new, _ws_arg(ws, dev)[0],
-        _stream_on(stream, dev)))
-
-
-def _paged_fits(desc: LayerDesc, cache: PagedCache):
-    if cache.Hkv != desc.c.Hkv or cache.B != desc.c.B:
-        raise ValueError(f"a cache of {cache.Hkv} KV heads and {cache.B} sequences does not go with "
-                         f"a description of {desc.c.Hkv} and {desc.c.B}")
+    return _check("rtp_paged_append_kv", (_lib._native or _lib.native()).append_kv(
+        desc.addr, cache.addr, cache.B, cache.Hkv, cache.device_index, k_pre, v, start_pos, slot_map,
+        n_new, ws, _stream_arg(stream)))
 
 
 def rtp_paged_decode_step(desc: LayerDesc, cache: PagedCache, q_pre, seq_lens, out, lse=None, ws=None,
                           stream=None):
     """Decode step of one layer over a paged cache (see include/rtp.h). q_pre, out: bf16
     [B][Hq][128]; seq_lens: int32 [B]; lse: float [B][Hq] or None."""
-    c, dev = desc.c, cache.device_index
-    _paged_fits(desc, cache)
-    n = c.B * c.Hq
-    w, wb = _ws_arg(ws, dev)
-    return _check("rtp_paged_decode_step", _lib.load().rtp_paged_decode_step(
-        desc.ref, cache.ref, _arg(q_pre, "q_pre", torch.bfloat16, n * 128, dev),
-        _arg(seq_lens, "seq_lens", torch.int32, c.B, dev),
-        _arg(out, "out", torch.bfloat16, n * 128, dev),
-        _arg(lse, "lse", torch.float32, n, dev, True), w, wb, _stream_on(stream, dev)))
+    c = _paged_fits(desc, cache)
+    return _check("rtp_paged_decode_step", (_lib._native or _lib.native()).decode_step(
+        desc.addr, cache.addr, cache.B, c.Hq, cache.Hkv, cache.device_index, None, None, q_pre,
+        seq_lens, out, lse, ws, _stream_arg(stream)))
 
 
 def rtp_paged_decode_step_append(desc: LayerDesc, cache: PagedCache, k_new, v_new, q_pre, seq_lens,
                                  out, lse=None, ws=None, stream=None):
     """The decode token's append and the decode step in one launch (see include/rtp.h). k_new,
     v_new: bf16 [B][Hkv][128]; the others as rtp_paged_decode_step."""
-    c, dev = desc.c, cache.device_index
-    _paged_fits(desc, cache)
-    n, m = c.B * c.Hq, c.B * c.Hkv * 128
-    w, wb = _ws_arg(ws, dev)
-    return _check("rtp_paged_decode_step_append", _lib.load().rtp_paged_decode_step_append(
-        desc.ref, cache.ref, _arg(k_new, "k_new", torch.bfloat16, m, dev),
-        _arg(v_new, "v_new", torch.bfloat16, m, dev),
-        _arg(q_pre, "q_pre", torch.bfloat16, n * 128, dev),
-        _arg(seq_lens, "seq_lens", torch.int32, c.B, dev),
-        _arg(out, "out", torch.bfloat16, n * 128, dev),
-        _arg(lse, "lse", torch.float32, n, dev, True), w, wb, _stream_on(stream, dev)))
+    c = _paged_fits(desc, cache)
+    if k_new is None or v_new is None:
+        raise ValueError("k_new and v_new: tensors are wanted")
+    return _check("rtp_paged_decode_step_append", (_lib._native or _lib.native()).decode_step(
+        desc.addr, cache.addr, cache.B, c.Hq, cache.Hkv, cache.device_index, k_new, v_new, q_pre,
+        seq_lens, out, lse, ws, _stream_arg(stream)))
 
 
 def rtp_decode_step_static(desc: LayerDesc, cache: RtpCache, q_pre, w_qidx, seq_lens, p, out,
