@@ -14,6 +14,12 @@
 // in shared memory, and what remains open at a CTA's two ends goes to the workspace, where the
 // CTA that arrives last at a group merges its parts in the order of the line (no waits, and the
 // result does not depend on who is last).
+//
+// Measured (8 KV heads of 4 query heads, all dense; launches back to back): 1M tokens in bf16
+// 627 us, 6.85 TB/s (without the arithmetic 609 us); 4 x 128K tokens in e4m3 187 us, 5.9 TB/s
+// (173 us). Under a load of seconds the power limit takes the clock from 1965 to about 1700 MHz,
+// and e4m3 follows it: 215 us. One sequence of 4K tokens takes 11 us: the chain of lengths, page
+// ids, rows, two joins and an arrival, each a trip to L2 or memory.
 #pragma once
 
 #include "rtp_attend.cuh"
@@ -51,6 +57,10 @@ struct PagedDecodeParams {
   float *part, *head;            // [ranges][2] partials of ranges, [CTAs][16] of warps
 };
 
+// bf16 rows: 8 warps with three tiles each, 192 KB of copies in the rings; the query's terms alone
+// are 48 registers a thread. (12 warps with two tiles each: 3 % slower on short sequences.)
+// e4m3 rows: their conversions keep the SM busy, so more warps: 12 with four tiles each, 187 us at
+// 4 x 131072 tokens of 8 KV heads; 8 warps 248 us, 16 warps (128 registers, some spilled) 191 us.
 template <int KV> struct PagedCfg;
 template <> struct PagedCfg<kKvBf16> {
   static constexpr int kWarps = 8, kStages = 3, kRowB = 256, kTerms = 3;
@@ -63,9 +73,9 @@ template <> struct PagedCfg<kKvE4m3> {
   static constexpr bool kLater = false;
 };
 
-
 constexpr int kPagedMaxWarps = 16;
-// Tiles' worth of a group's fixed cost (query, angles, output) in the split of the line
+// Tiles' worth of a group's fixed cost (query, angles, output) in the split of the line: 256
+// sequences of 0 to 1024 tokens took 145 us without it, 115 us with 3 (and with 8)
 constexpr int kSetup = 3;
 static_assert(kSetup > 0, "an empty sequence is divided by its places");
 
@@ -952,354 +962,354 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams P) {
 
 #pragma unroll 1
   while (true) {
-  const int len = (int)(ct1 - ct0);                    // below 2^31: a sequence has 2^26 places at most
-  // this warp's places, counted from ct0
-  int line = (int)((long long)warp * len / NW);        // place of the tile at cc
-  const int p1 = (int)((long long)(warp + 1) * len / NW);
-  Cursor cc;
-  if (line < p1) {
-    const long long p0 = ct0 + line;
-    if (nc > 1) {
-      int before = 0;                                  // chunks that start at or before p0
-      for (int i = lane; i < nc; i += 32) before += prefix[i] <= p0;
-      chunk = __reduce_add_sync(0xffffffffu, before) - 1;
-      base = prefix[chunk];
+    const int len = (int)(ct1 - ct0);                    // below 2^31: a sequence has 2^26 places at most
+    // this warp's places, counted from ct0
+    int line = (int)((long long)warp * len / NW);        // place of the tile at cc
+    const int p1 = (int)((long long)(warp + 1) * len / NW);
+    Cursor cc;
+    if (line < p1) {
+      const long long p0 = ct0 + line;
+      if (nc > 1) {
+        int before = 0;                                  // chunks that start at or before p0
+        for (int i = lane; i < nc; i += 32) before += prefix[i] <= p0;
+        chunk = __reduce_add_sync(0xffffffffu, before) - 1;
+        base = prefix[chunk];
+      }
+      if (nc > 1 || (Cfg::kLater && range != blockIdx.x)) {
+        lens = paged_len(P, chunk * 32 + lane, nullptr);
+        mine = seq_places(L, lens);
+        incl = warp_incl_sum(mine);
+      }
+      int skip;
+      cc = cursor_at(P, chunk, p0 - base, lens, incl, mine, &skip);
+      line += skip;
     }
-    if (nc > 1 || (Cfg::kLater && range != blockIdx.x)) {
-      lens = paged_len(P, chunk * 32 + lane, nullptr);
-      mine = seq_places(L, lens);
-      incl = warp_incl_sum(mine);
-    }
-    int skip;
-    cc = cursor_at(P, chunk, p0 - base, lens, incl, mine, &skip);
-    line += skip;
-  }
-  __syncthreads();                                     // theta, ent
+    __syncthreads();                                     // theta, ent
 
-  PagedAttn<KV> A;
-  if (line < p1) {
-    Cursor pc = cc;
-    int pline = line;                                  // place of the tile at pc, the next to copy
-    // fill the ring: the page ids of its tiles are loaded together, and the first query and its
-    // angles meanwhile
-    TileDesc d[NS];
-    bool have[NS];
+    PagedAttn<KV> A;
+    if (line < p1) {
+      Cursor pc = cc;
+      int pline = line;                                  // place of the tile at pc, the next to copy
+      // fill the ring: the page ids of its tiles are loaded together, and the first query and its
+      // angles meanwhile
+      TileDesc d[NS];
+      bool have[NS];
 #pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      have[s] = pline < p1;
-      if (have[s]) {
-        d[s] = tile_desc(P, pc);
-        cursor_step(P, pc, pline);
-      }
-    }
-    QueryRaw qr;
-    query_fetch<KV>(P, qr, cc.b, kv_head(L, cc.gi));
-    fill_angles(theta, ang, cc.n - 1);
-#pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      if (have[s]) tile_issue<KV>(P, d[s], ring_s + s * Cfg::kStageB, masks + s);
-      cp_async_commit();
-    }
-    TileDesc nx;                                       // the next tile, its page id on the way
-    bool more = pline < p1;
-    if (more) {
-      nx = tile_desc(P, pc);
-      cursor_step(P, pc, pline);
-    }
-    query_terms<KV>(A, qr, ang, G);
-    attn_reset<KV>(A);
-    int seg_k = cc.k, ang_b = cc.b, slot = 0;
-    bool has_head = false, fresh = false;
-#pragma unroll 1
-    while (line < p1) {
-      const int kvh = kv_head(L, cc.gi);
-      if (fresh) {                                     // first tile of a group
-        QueryRaw q2;
-        query_fetch<KV>(P, q2, cc.b, kvh);
-        if (cc.b != ang_b) {
-          fill_angles(theta, ang, cc.n - 1);
-          ang_b = cc.b;
-        }
-        query_terms<KV>(A, q2, ang, G);
-        attn_reset<KV>(A);
-        seg_k = 0;
-        fresh = false;
-      }
-      cp_async_wait<NS - 1>();
-      __syncwarp();
-      const uint32_t stage = ring_s + slot * Cfg::kStageB;
-      const uint32_t mask = masks[slot];
-      if (APPEND && cc.k == cc.nt - 1 && mask) {       // the last tile holds the new token's row
-        const int pos = cc.n - 1;
-        const int pid = __ldg(P.C.table + (int64_t)cc.b * P.C.table_stride + (pos >> P.C.lg));
-        const int in = (kvh << P.C.lg) + (pos & ((1 << P.C.lg) - 1));
-        paged_append_row<KV>(P, theta, cc.b, kvh, pos, pid * P.C.page_stride + in,
-                             pid * (L.Hkv << P.C.lg) + in, stage);
-      }
-      paged_tile<KV>(A, stage, mask);
-      __syncwarp();
-      if (more) {
-        tile_issue<KV>(P, nx, stage, masks + slot);
-        more = pline < p1;
-        if (more) {
-          nx = tile_desc(P, pc);
+      for (int s = 0; s < NS; ++s) {
+        have[s] = pline < p1;
+        if (have[s]) {
+          d[s] = tile_desc(P, pc);
           cursor_step(P, pc, pline);
         }
       }
-      cp_async_commit();
-      if (++slot == NS) slot = 0;
-      ++cc.k;
-      ++line;
-      const bool ends = cc.k == cc.nt;
-      const bool last = line + (ends ? kSetup : 0) >= p1;
-      if (ends || last) {
-        attn_sum<KV>(A);
-        const bool starts = seg_k == 0;
-        if (starts && ends) {
-          attn_write<KV>(P, A, cc.b, kvh);
-        } else {
-          // an open end: to the drained ring, or, where tiles of other groups follow and the ring
-          // is in use, to the workspace for now (then it is of a group that an earlier warp began)
-          float* dst = reinterpret_cast<float*>(ring) + (starts ? warp_part_floats(G) : 0);
-          if (!last) {
-            dst = P.head + (int64_t)(blockIdx.x * NW + warp) * warp_part_floats(G);
-            has_head = true;
-          } else {
-            cp_async_wait<0>();
-            __syncwarp();
+      QueryRaw qr;
+      query_fetch<KV>(P, qr, cc.b, kv_head(L, cc.gi));
+      fill_angles(theta, ang, cc.n - 1);
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        if (have[s]) tile_issue<KV>(P, d[s], ring_s + s * Cfg::kStageB, masks + s);
+        cp_async_commit();
+      }
+      TileDesc nx;                                       // the next tile, its page id on the way
+      bool more = pline < p1;
+      if (more) {
+        nx = tile_desc(P, pc);
+        cursor_step(P, pc, pline);
+      }
+      query_terms<KV>(A, qr, ang, G);
+      attn_reset<KV>(A);
+      int seg_k = cc.k, ang_b = cc.b, slot = 0;
+      bool has_head = false, fresh = false;
+#pragma unroll 1
+      while (line < p1) {
+        const int kvh = kv_head(L, cc.gi);
+        if (fresh) {                                     // first tile of a group
+          QueryRaw q2;
+          query_fetch<KV>(P, q2, cc.b, kvh);
+          if (cc.b != ang_b) {
+            fill_angles(theta, ang, cc.n - 1);
+            ang_b = cc.b;
           }
-          attn_store<KV>(A, dst, G);
-          if (lane == 0) {
-            PagedEntry e;
-            e.gid = cc.b * L.Hkv + cc.gi;
-            e.ge = ct0 + line + (cc.nt - cc.k);
-            e.gs = e.ge - cc.nt;
-            e.pad = 0;
-            ent[2 * warp + (starts ? 1 : 0)] = e;
+          query_terms<KV>(A, q2, ang, G);
+          attn_reset<KV>(A);
+          seg_k = 0;
+          fresh = false;
+        }
+        cp_async_wait<NS - 1>();
+        __syncwarp();
+        const uint32_t stage = ring_s + slot * Cfg::kStageB;
+        const uint32_t mask = masks[slot];
+        if (APPEND && cc.k == cc.nt - 1 && mask) {       // the last tile holds the new token's row
+          const int pos = cc.n - 1;
+          const int pid = __ldg(P.C.table + (int64_t)cc.b * P.C.table_stride + (pos >> P.C.lg));
+          const int in = (kvh << P.C.lg) + (pos & ((1 << P.C.lg) - 1));
+          paged_append_row<KV>(P, theta, cc.b, kvh, pos, pid * P.C.page_stride + in,
+                               pid * (L.Hkv << P.C.lg) + in, stage);
+        }
+        paged_tile<KV>(A, stage, mask);
+        __syncwarp();
+        if (more) {
+          tile_issue<KV>(P, nx, stage, masks + slot);
+          more = pline < p1;
+          if (more) {
+            nx = tile_desc(P, pc);
+            cursor_step(P, pc, pline);
           }
         }
-        if (ends) {
-          line += kSetup;
-          if (!last) cursor_next_group(P, cc);
-          fresh = true;
+        cp_async_commit();
+        if (++slot == NS) slot = 0;
+        ++cc.k;
+        ++line;
+        const bool ends = cc.k == cc.nt;
+        const bool last = line + (ends ? kSetup : 0) >= p1;
+        if (ends || last) {
+          attn_sum<KV>(A);
+          const bool starts = seg_k == 0;
+          if (starts && ends) {
+            attn_write<KV>(P, A, cc.b, kvh);
+          } else {
+            // an open end: to the drained ring, or, where tiles of other groups follow and the ring
+            // is in use, to the workspace for now (then it is of a group that an earlier warp began)
+            float* dst = reinterpret_cast<float*>(ring) + (starts ? warp_part_floats(G) : 0);
+            if (!last) {
+              dst = P.head + (int64_t)(blockIdx.x * NW + warp) * warp_part_floats(G);
+              has_head = true;
+            } else {
+              cp_async_wait<0>();
+              __syncwarp();
+            }
+            attn_store<KV>(A, dst, G);
+            if (lane == 0) {
+              PagedEntry e;
+              e.gid = cc.b * L.Hkv + cc.gi;
+              e.ge = ct0 + line + (cc.nt - cc.k);
+              e.gs = e.ge - cc.nt;
+              e.pad = 0;
+              ent[2 * warp + (starts ? 1 : 0)] = e;
+            }
+          }
+          if (ends) {
+            line += kSetup;
+            if (!last) cursor_next_group(P, cc);
+            fresh = true;
+          }
+        }
+      }
+      cp_async_wait<0>();
+      __syncwarp();
+      if (has_head) {
+        const float4* src = reinterpret_cast<const float4*>(
+            P.head + (int64_t)(blockIdx.x * NW + warp) * warp_part_floats(G));
+#pragma unroll 9
+        for (int i = lane; i < warp_part_floats(G) / 4; i += 32)
+          reinterpret_cast<float4*>(ring)[i] = src[i];
+      }
+    }
+    __syncthreads();
+
+    // ---- the open ends of this CTA's warps: the entries of a group (a run) are merged in the order
+    // of the line, one (run, head) a warp. (The code is kept small: it runs once, and most of its
+    // time is that of fetching its instructions.)
+    int open_run[2] = {-1, -1};                          // first entry of the groups left open
+    {
+      const int gid = lane < 2 * NW ? ent[lane].gid : -1;
+      const uint32_t valid = __ballot_sync(0xffffffffu, gid >= 0), below = valid & ((1u << lane) - 1);
+      const int before = __shfl_sync(0xffffffffu, gid, below ? 31 - __clz(below) : 0);
+      const bool lead = gid >= 0 && (!below || before != gid);
+      const uint32_t leads = __ballot_sync(0xffffffffu, lead);
+      const PagedEntry* mine_e = ent + min(lane, 2 * NW - 1);
+      const uint32_t left = __ballot_sync(0xffffffffu, lead && mine_e->gs < ct0);
+      const uint32_t right = __ballot_sync(0xffffffffu, lead && mine_e->ge > ct1) & ~left;
+      if (left) open_run[0] = __ffs(left) - 1;
+      if (right) open_run[1] = __ffs(right) - 1;
+      int unit = 0;                                      // (at most 32 runs of 8 heads)
+#pragma unroll 1
+      for (uint32_t todo = leads; todo; unit += G) {
+        const int first = __ffs(todo) - 1;
+        uint32_t members = valid & ~((1u << first) - 1);
+        todo &= todo - 1;
+        if (todo) members &= (1u << (__ffs(todo) - 1)) - 1;
+#pragma unroll 1
+        for (int h = (warp + 64 * NW - unit) % NW; h < G; h += NW) {
+          float M = -INFINITY, MO = -INFINITY, Ls = 0.f;
+          float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+          for (uint32_t mem = members; mem; mem &= mem - 1) {
+            const float* q = entry_part(__ffs(mem) - 1) + G * kPartPitch + 3 * h;
+            M = fmaxf(M, q[0]);
+            MO = fmaxf(MO, q[2]);
+          }
+#pragma unroll 1
+          for (uint32_t mem = members; mem; mem &= mem - 1) {
+            const float* q = entry_part(__ffs(mem) - 1);
+            const float4 a = *reinterpret_cast<const float4*>(q + h * kPartPitch + 4 * lane);
+            q += G * kPartPitch + 3 * h;
+            const float w = ex2_from(q[2], MO);
+            Ls += q[1] * ex2_from(q[0], M);
+            s.x = fmaf(a.x, w, s.x); s.y = fmaf(a.y, w, s.y);
+            s.z = fmaf(a.z, w, s.z); s.w = fmaf(a.w, w, s.w);
+          }
+          if (first != open_run[0] && first != open_run[1]) {
+            const int gd = ent[first].gid, b = small_div(gd, L.Hkv);
+            const int64_t head = (int64_t)b * L.Hq + (int64_t)kv_head(L, gd - b * L.Hkv) * G + h;
+            const float f = Ls > 0.f || Ls != Ls ? ex2_from(MO, M) / Ls : 0.f;
+            uint2 w;
+            w.x = pack_bf2(s.x * f, s.y * f);
+            w.y = pack_bf2(s.z * f, s.w * f);
+            *reinterpret_cast<uint2*>(P.out + head * kD + 4 * lane) = w;
+            if (P.lse && lane == 0) P.lse[head] = (M + log2f(Ls)) * 0.6931471805599453f;
+          } else {
+            float* gp = P.part + (int64_t)((Cfg::kLater ? range : (int)blockIdx.x) * 2 + (first == open_run[0] ? 0 : 1)) * cta_part_floats(G);
+            *reinterpret_cast<float4*>(gp + h * kD + 4 * lane) = s;
+            if (lane < 3) gp[G * kD + 3 * h + lane] = lane == 0 ? M : lane == 1 ? Ls : MO;
+          }
         }
       }
     }
-    cp_async_wait<0>();
-    __syncwarp();
-    if (has_head) {
-      const float4* src = reinterpret_cast<const float4*>(
-          P.head + (int64_t)(blockIdx.x * NW + warp) * warp_part_floats(G));
-#pragma unroll 9
-      for (int i = lane; i < warp_part_floats(G) / 4; i += 32)
-        reinterpret_cast<float4*>(ring)[i] = src[i];
-    }
-  }
-  __syncthreads();
+    if (open_run[0] >= 0 || open_run[1] >= 0) {
+      __syncthreads();
+      // a group that spans ranges c0..c1 counts its arrivals at c0's word, which wraps to zero
+      int* finish = reinterpret_cast<int*>(sm + S::kMisc);
+      if (tid < 2) {
+        const int first = tid ? open_run[1] : open_run[0];
+        int last = 0;
+        if (first >= 0) {
+          const PagedEntry e = ent[first];
+          const int c0 = range_of<Cfg::kLater>(split, e.gs), c1 = range_of<Cfg::kLater>(split, e.ge - 1);
+          // the CTA's partial before the arrival, the others' after it
+          uint32_t old;
+          asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;"
+                       : "=r"(old) : "l"(P.arrive + c0), "r"((uint32_t)(c1 - c0)) : "memory");
+          last = old == (uint32_t)(c1 - c0);
+        }
+        finish[tid] = last;
+      }
+      __syncthreads();
 
-  // ---- the open ends of this CTA's warps: the entries of a group (a run) are merged in the order
-  // of the line, one (run, head) a warp. (The code is kept small: it runs once, and most of its
-  // time is that of fetching its instructions.)
-  int open_run[2] = {-1, -1};                          // first entry of the groups left open
-  {
-    const int gid = lane < 2 * NW ? ent[lane].gid : -1;
-    const uint32_t valid = __ballot_sync(0xffffffffu, gid >= 0), below = valid & ((1u << lane) - 1);
-    const int before = __shfl_sync(0xffffffffu, gid, below ? 31 - __clz(below) : 0);
-    const bool lead = gid >= 0 && (!below || before != gid);
-    const uint32_t leads = __ballot_sync(0xffffffffu, lead);
-    const PagedEntry* mine_e = ent + min(lane, 2 * NW - 1);
-    const uint32_t left = __ballot_sync(0xffffffffu, lead && mine_e->gs < ct0);
-    const uint32_t right = __ballot_sync(0xffffffffu, lead && mine_e->ge > ct1) & ~left;
-    if (left) open_run[0] = __ffs(left) - 1;
-    if (right) open_run[1] = __ffs(right) - 1;
-    int unit = 0;                                      // (at most 32 runs of 8 heads)
+      // ---- groups at which this CTA was the last to arrive
+      float* wt = reinterpret_cast<float*>(sm + S::kWt);          // [parts][8]
+      float* fac = reinterpret_cast<float*>(sm + S::kMisc) + 16;  // [8]
+      const int items = G * (kD / 4);
+      const int64_t pf = cta_part_floats(G);
+      for (int x = 0; x < 2; ++x) {
+        if (!finish[x]) continue;
+        const PagedEntry e = ent[x ? open_run[1] : open_run[0]];
+        const int c0 = range_of<Cfg::kLater>(split, e.gs), np = range_of<Cfg::kLater>(split, e.ge - 1) - c0 + 1;
+        // part i: the open end of range c0 + i (its last group for i = 0, its first otherwise)
+        const float* part = P.part + (int64_t)c0 * 2 * pf;
+        const int b = small_div(e.gid, L.Hkv);
+        const int64_t head0 = (int64_t)b * L.Hq + (int64_t)kv_head(L, e.gid - b * L.Hkv) * G;
+        // Four channels a thread; where G is small, teams of threads share out the parts.
+        // As many parts as the rings hold are copied to shared memory, all copies in flight at once
+        // (loads into registers, 8 at a time, took 9 us for 103 parts), while the weights are made.
+        const int pb = (int)pf * 4, fit = S::kRing / pb;
+        const unsigned char* part_b = reinterpret_cast<const unsigned char*>(part);
+        const int teams = NT / items, team = tid / items, it = tid - team * items, h = it >> 5;
+        auto copy = [&](int i0, int nb) {                  // a thread copies the 16 bytes it sums up
+          if (team < teams)
+            for (int i = i0 + team; i < i0 + nb; i += teams)
+              cp_async16(sm + (i - i0) * pb + it * 16, part_b + (int64_t)(i * 2 + (i == 0)) * pb + it * 16);
+          cp_async_commit();
+        };
+        copy(0, min(np, fit));
+        if (warp < G) {
+          // up to 160 parts (all, but for one group over a long line) from registers
+          constexpr int kHeld = kPagedMaxCTAs / 32;
+          float m[kHeld], l[kHeld], mo[kHeld];
+          float M = -INFINITY, MO = -INFINITY, Ls = 0.f;
+          auto state = [&](int i) { return part + (i * 2 + (i == 0)) * pf + G * kD + 3 * warp; };
+#pragma unroll
+          for (int u = 0; u < kHeld; ++u) {
+            const int i = lane + 32 * u;
+            m[u] = i < np ? __ldcg(state(i)) : -INFINITY;
+            l[u] = i < np ? __ldcg(state(i) + 1) : 0.f;
+            mo[u] = i < np ? __ldcg(state(i) + 2) : -INFINITY;
+          }
+#pragma unroll
+          for (int u = 0; u < kHeld; ++u) { M = fmaxf(M, m[u]); MO = fmaxf(MO, mo[u]); }
+          if (Cfg::kLater)
 #pragma unroll 1
-    for (uint32_t todo = leads; todo; unit += G) {
-      const int first = __ffs(todo) - 1;
-      uint32_t members = valid & ~((1u << first) - 1);
-      todo &= todo - 1;
-      if (todo) members &= (1u << (__ffs(todo) - 1)) - 1;
+            for (int i = lane + 32 * kHeld; i < np; i += 32) {
+              M = fmaxf(M, __ldcg(state(i)));
+              MO = fmaxf(MO, __ldcg(state(i) + 2));
+            }
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) {
+            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+            MO = fmaxf(MO, __shfl_xor_sync(0xffffffffu, MO, o));
+          }
+#pragma unroll
+          for (int u = 0; u < kHeld; ++u) {
+            const int i = lane + 32 * u;
+            if (i < np) {
+              Ls += l[u] * ex2_from(m[u], M);
+              wt[i * 8 + warp] = ex2_from(mo[u], MO);
+            }
+          }
+          if (Cfg::kLater)
 #pragma unroll 1
-      for (int h = (warp + 64 * NW - unit) % NW; h < G; h += NW) {
-        float M = -INFINITY, MO = -INFINITY, Ls = 0.f;
+            for (int i = lane + 32 * kHeld; i < np; i += 32) {
+              Ls += __ldcg(state(i) + 1) * ex2_from(__ldcg(state(i)), M);
+              wt[i * 8 + warp] = ex2_from(__ldcg(state(i) + 2), MO);
+            }
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) Ls += __shfl_xor_sync(0xffffffffu, Ls, o);
+          if (lane == 0) {
+            fac[warp] = Ls > 0.f || Ls != Ls ? ex2_from(MO, M) / Ls : 0.f;
+            if (P.lse) P.lse[head0 + warp] = (M + log2f(Ls)) * 0.6931471805599453f;
+          }
+        }
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-        for (uint32_t mem = members; mem; mem &= mem - 1) {
-          const float* q = entry_part(__ffs(mem) - 1) + G * kPartPitch + 3 * h;
-          M = fmaxf(M, q[0]);
-          MO = fmaxf(MO, q[2]);
+        for (int i0 = 0; i0 < np; i0 += fit) {
+          if (i0 > 0) {
+            __syncthreads();
+            copy(i0, min(np - i0, fit));
+          }
+          cp_async_wait<0>();
+          __syncthreads();
+          if (team < teams) {
+            const int end = min(np, i0 + fit);
+#pragma unroll 4
+            for (int i = i0 + team; i < end; i += teams) {
+              const float4 a = *reinterpret_cast<const float4*>(sm + (i - i0) * pb + it * 16);
+              const float w = wt[i * 8 + h];
+              s.x = fmaf(a.x, w, s.x); s.y = fmaf(a.y, w, s.y);
+              s.z = fmaf(a.z, w, s.z); s.w = fmaf(a.w, w, s.w);
+            }
+          }
         }
-#pragma unroll 1
-        for (uint32_t mem = members; mem; mem &= mem - 1) {
-          const float* q = entry_part(__ffs(mem) - 1);
-          const float4 a = *reinterpret_cast<const float4*>(q + h * kPartPitch + 4 * lane);
-          q += G * kPartPitch + 3 * h;
-          const float w = ex2_from(q[2], MO);
-          Ls += q[1] * ex2_from(q[0], M);
-          s.x = fmaf(a.x, w, s.x); s.y = fmaf(a.y, w, s.y);
-          s.z = fmaf(a.z, w, s.z); s.w = fmaf(a.w, w, s.w);
-        }
-        if (first != open_run[0] && first != open_run[1]) {
-          const int gd = ent[first].gid, b = small_div(gd, L.Hkv);
-          const int64_t head = (int64_t)b * L.Hq + (int64_t)kv_head(L, gd - b * L.Hkv) * G + h;
-          const float f = Ls > 0.f || Ls != Ls ? ex2_from(MO, M) / Ls : 0.f;
+        __syncthreads();
+        float4* red = reinterpret_cast<float4*>(sm);
+        red[tid] = s;
+        __syncthreads();
+        if (tid < items) {
+          for (int q = 1; q < teams; ++q) {
+            const float4 a = red[q * items + it];
+            s.x += a.x; s.y += a.y; s.z += a.z; s.w += a.w;
+          }
+          const float f = fac[h];
           uint2 w;
           w.x = pack_bf2(s.x * f, s.y * f);
           w.y = pack_bf2(s.z * f, s.w * f);
-          *reinterpret_cast<uint2*>(P.out + head * kD + 4 * lane) = w;
-          if (P.lse && lane == 0) P.lse[head] = (M + log2f(Ls)) * 0.6931471805599453f;
-        } else {
-          float* gp = P.part + (int64_t)((Cfg::kLater ? range : (int)blockIdx.x) * 2 + (first == open_run[0] ? 0 : 1)) * cta_part_floats(G);
-          *reinterpret_cast<float4*>(gp + h * kD + 4 * lane) = s;
-          if (lane < 3) gp[G * kD + 3 * h + lane] = lane == 0 ? M : lane == 1 ? Ls : MO;
+          *reinterpret_cast<uint2*>(P.out + head0 * kD + 4 * it) = w;
         }
-      }
-    }
-  }
-  if (open_run[0] >= 0 || open_run[1] >= 0) {
-  __syncthreads();
-  // a group that spans ranges c0..c1 counts its arrivals at c0's word, which wraps to zero
-  int* finish = reinterpret_cast<int*>(sm + S::kMisc);
-  if (tid < 2) {
-    const int first = tid ? open_run[1] : open_run[0];
-    int last = 0;
-    if (first >= 0) {
-      const PagedEntry e = ent[first];
-      const int c0 = range_of<Cfg::kLater>(split, e.gs), c1 = range_of<Cfg::kLater>(split, e.ge - 1);
-      // the CTA's partial before the arrival, the others' after it
-      uint32_t old;
-      asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;"
-                   : "=r"(old) : "l"(P.arrive + c0), "r"((uint32_t)(c1 - c0)) : "memory");
-      last = old == (uint32_t)(c1 - c0);
-    }
-    finish[tid] = last;
-  }
-  __syncthreads();
-
-  // ---- groups at which this CTA was the last to arrive
-  float* wt = reinterpret_cast<float*>(sm + S::kWt);          // [parts][8]
-  float* fac = reinterpret_cast<float*>(sm + S::kMisc) + 16;  // [8]
-  const int items = G * (kD / 4);
-  const int64_t pf = cta_part_floats(G);
-  for (int x = 0; x < 2; ++x) {
-    if (!finish[x]) continue;
-    const PagedEntry e = ent[x ? open_run[1] : open_run[0]];
-    const int c0 = range_of<Cfg::kLater>(split, e.gs), np = range_of<Cfg::kLater>(split, e.ge - 1) - c0 + 1;
-    // part i: the open end of range c0 + i (its last group for i = 0, its first otherwise)
-    const float* part = P.part + (int64_t)c0 * 2 * pf;
-    const int b = small_div(e.gid, L.Hkv);
-    const int64_t head0 = (int64_t)b * L.Hq + (int64_t)kv_head(L, e.gid - b * L.Hkv) * G;
-    // Four channels a thread; where G is small, teams of threads share out the parts.
-    // As many parts as the rings hold are copied to shared memory, all copies in flight at once
-    // (loads into registers, 8 at a time, took 9 us for 103 parts), while the weights are made.
-    const int pb = (int)pf * 4, fit = S::kRing / pb;
-    const unsigned char* part_b = reinterpret_cast<const unsigned char*>(part);
-    const int teams = NT / items, team = tid / items, it = tid - team * items, h = it >> 5;
-    auto copy = [&](int i0, int nb) {                  // a thread copies the 16 bytes it sums up
-      if (team < teams)
-        for (int i = i0 + team; i < i0 + nb; i += teams)
-          cp_async16(sm + (i - i0) * pb + it * 16, part_b + (int64_t)(i * 2 + (i == 0)) * pb + it * 16);
-      cp_async_commit();
-    };
-    copy(0, min(np, fit));
-    if (warp < G) {
-      // up to 160 parts (all, but for one group over a long line) from registers
-      constexpr int kHeld = kPagedMaxCTAs / 32;
-      float m[kHeld], l[kHeld], mo[kHeld];
-      float M = -INFINITY, MO = -INFINITY, Ls = 0.f;
-      auto state = [&](int i) { return part + (i * 2 + (i == 0)) * pf + G * kD + 3 * warp; };
-#pragma unroll
-      for (int u = 0; u < kHeld; ++u) {
-        const int i = lane + 32 * u;
-        m[u] = i < np ? __ldcg(state(i)) : -INFINITY;
-        l[u] = i < np ? __ldcg(state(i) + 1) : 0.f;
-        mo[u] = i < np ? __ldcg(state(i) + 2) : -INFINITY;
-      }
-#pragma unroll
-      for (int u = 0; u < kHeld; ++u) { M = fmaxf(M, m[u]); MO = fmaxf(MO, mo[u]); }
-      if (Cfg::kLater)
-#pragma unroll 1
-        for (int i = lane + 32 * kHeld; i < np; i += 32) {
-          M = fmaxf(M, __ldcg(state(i)));
-          MO = fmaxf(MO, __ldcg(state(i) + 2));
-        }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        MO = fmaxf(MO, __shfl_xor_sync(0xffffffffu, MO, o));
-      }
-#pragma unroll
-      for (int u = 0; u < kHeld; ++u) {
-        const int i = lane + 32 * u;
-        if (i < np) {
-          Ls += l[u] * ex2_from(m[u], M);
-          wt[i * 8 + warp] = ex2_from(mo[u], MO);
-        }
-      }
-      if (Cfg::kLater)
-#pragma unroll 1
-        for (int i = lane + 32 * kHeld; i < np; i += 32) {
-          Ls += __ldcg(state(i) + 1) * ex2_from(__ldcg(state(i)), M);
-          wt[i * 8 + warp] = ex2_from(__ldcg(state(i) + 2), MO);
-        }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) Ls += __shfl_xor_sync(0xffffffffu, Ls, o);
-      if (lane == 0) {
-        fac[warp] = Ls > 0.f || Ls != Ls ? ex2_from(MO, M) / Ls : 0.f;
-        if (P.lse) P.lse[head0 + warp] = (M + log2f(Ls)) * 0.6931471805599453f;
-      }
-    }
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = 0; i0 < np; i0 += fit) {
-      if (i0 > 0) {
         __syncthreads();
-        copy(i0, min(np - i0, fit));
-      }
-      cp_async_wait<0>();
-      __syncthreads();
-      if (team < teams) {
-        const int end = min(np, i0 + fit);
-#pragma unroll 4
-        for (int i = i0 + team; i < end; i += teams) {
-          const float4 a = *reinterpret_cast<const float4*>(sm + (i - i0) * pb + it * 16);
-          const float w = wt[i * 8 + h];
-          s.x = fmaf(a.x, w, s.x); s.y = fmaf(a.y, w, s.y);
-          s.z = fmaf(a.z, w, s.z); s.w = fmaf(a.w, w, s.w);
-        }
       }
     }
-    __syncthreads();
-    float4* red = reinterpret_cast<float4*>(sm);
-    red[tid] = s;
-    __syncthreads();
-    if (tid < items) {
-      for (int q = 1; q < teams; ++q) {
-        const float4 a = red[q * items + it];
-        s.x += a.x; s.y += a.y; s.z += a.z; s.w += a.w;
-      }
-      const float f = fac[h];
-      uint2 w;
-      w.x = pack_bf2(s.x * f, s.y * f);
-      w.y = pack_bf2(s.z * f, s.w * f);
-      *reinterpret_cast<uint2*>(P.out + head0 * kD + 4 * it) = w;
+    if (!Cfg::kLater || later == 0) return;
+    // ---- the next range that nobody has taken; each CTA comes here once too often, so the count
+    // wraps to zero
+    __syncthreads();                                     // the rings and entries are free
+    if (tid == 0) {
+      const uint32_t old = atomicInc(P.queue, (uint32_t)(split.n + later - 1));
+      *next_range = old < (uint32_t)later ? split.n + (int)old : -1;
     }
+    if (tid < 2 * NW) ent[tid].gid = -1;
     __syncthreads();
-  }
-  }
-  if (!Cfg::kLater || later == 0) return;
-  // ---- the next range that nobody has taken; each CTA comes here once too often, so the count
-  // wraps to zero
-  __syncthreads();                                     // the rings and entries are free
-  if (tid == 0) {
-    const uint32_t old = atomicInc(P.queue, (uint32_t)(split.n + later - 1));
-    *next_range = old < (uint32_t)later ? split.n + (int)old : -1;
-  }
-  if (tid < 2 * NW) ent[tid].gid = -1;
-  __syncthreads();
-  range = *next_range;
-  if (range < 0) return;
-  ct0 = range_start<Cfg::kLater>(split, range);
-  ct1 = range_start<Cfg::kLater>(split, range + 1);
+    range = *next_range;
+    if (range < 0) return;
+    ct0 = range_start<Cfg::kLater>(split, range);
+    ct1 = range_start<Cfg::kLater>(split, range + 1);
   }
 }
 

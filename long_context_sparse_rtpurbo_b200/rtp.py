@@ -172,8 +172,10 @@ class PagedCache:
             raise ValueError("k and v: [n_pages][Hkv][page_size][128] tensors of equal strides")
         n_pages, Hkv, page, _ = k.shape
         block = Hkv * page
-        if k.stride()[1:] != (page * 128, 128, 1) or (n_pages > 1 and k.stride(0) % 128):
-            raise ValueError("the rows of a page must be dense and pages a whole number of rows apart")
+        if k.stride()[1:] != (page * 128, 128, 1) or (
+                n_pages > 1 and (k.stride(0) % 128 or k.stride(0) < block * 128)):
+            raise ValueError("the rows of a page must be dense, and pages a whole number of rows "
+                             "apart that do not overlap")
         e4m3 = k.dtype in (torch.uint8, torch.float8_e4m3fn)
         if v.dtype is not k.dtype or not (e4m3 or k.dtype is torch.bfloat16):
             raise ValueError("k and v are both bfloat16, or both e4m3 (float8_e4m3fn or uint8)")

@@ -125,7 +125,9 @@ class Case:
         return out, lse
 
     def status(self):
-        return _mods()[2].rtp_read_device_status(self.ws)
+        st = _mods()[2].rtp_read_device_status(self.ws)
+        assert not self.ws[:4096].any()            # the counters are back at zero
+        return st
 
     def agree(self, out, lse, b, h, n, keep=None):
         """One head's outputs against the model over positions 0..n-1 (or `keep` of them)."""
@@ -228,6 +230,62 @@ def test_decode_largest_batch():
     out, lse = c.decode()
     assert c.status() == 0
     c.check(out, lse)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [639, 641, 960, 961])
+def test_decode_around_one_cta_per_group(n, kv):
+    """Lengths around those up to which a group stays in one CTA (40 and 60 tiles of 16 rows)."""
+    c = Case(n, [n, 0, 17, n - 1], 16, kv, G=2, Hkv=4, ret=(True, False, True, False), window=700)
+    out, lse = c.decode()
+    assert c.status() == 0
+    c.check(out, lse)
+
+
+@pytest.mark.parametrize("Hkv,n", [(1, 2_500_007), (8, 310_000)])
+def test_decode_longest_lines(Hkv, n):
+    """Lines long enough to leave a share to the CTAs that are done first: one group in some 300
+    parts, and eight groups. Against 64-bit sums on the GPU; three calls give the same bits,
+    whichever CTA took which part."""
+    _, _, rtp = _mods()
+    page, G = 128, 2
+    gen = torch.Generator(device=DEV).manual_seed(n)
+    n_pages = -(-n // page)
+    k, v = (torch.randn((n_pages, Hkv, page, 128), dtype=torch.bfloat16, device=DEV, generator=gen) for _ in range(2))
+    table = torch.randperm(n_pages, generator=gen, device=DEV).to(torch.int32)[None].contiguous()
+    q = (2 * torch.randn((1, G * Hkv, 128), device=DEV, generator=gen)).to(torch.bfloat16)
+    desc = rtp.LayerDesc(1, G * Hkv, Hkv, 0, 1, 1 << 22, rtp.rtp_build_slot_map([1] * Hkv)[0], BASE)
+    cache = rtp.make_paged_cache(k, v, table)
+    ws = torch.empty(rtp.rtp_paged_workspace_bytes(desc), dtype=torch.uint8, device=DEV)
+    rtp.rtp_paged_workspace_init(ws)
+    lens = torch.tensor([n], dtype=torch.int32, device=DEV)
+    outs = []
+    for _ in range(3):
+        out = torch.full((1, G * Hkv, 128), 7.0, dtype=torch.bfloat16, device=DEV)
+        lse = torch.full((1, G * Hkv), 7.0, device=DEV)
+        rtp.rtp_paged_decode_step(desc, cache, q, lens, out, lse, ws)
+        assert rtp.rtp_last_launch_count() == 1
+        outs.append((out, lse))
+    assert rtp.rtp_read_device_status(ws) == 0 and not ws[:4096].any()
+    for o, l in outs[1:]:
+        assert torch.equal(o, outs[0][0]) and torch.equal(l, outs[0][1])
+    q64 = torch.from_numpy(rope_rotate(_f64(q)[0], n - 1, BASE)).to(DEV)
+    for h in range(0, G * Hkv, 3):
+        K = k[table[0].long(), h // G].reshape(-1, 128)[:n].double()
+        S = (K.abs() @ q64[h].abs()).max().item() / 128 ** 0.5
+        z = K @ q64[h] / 128 ** 0.5
+        del K
+        V = v[table[0].long(), h // G].reshape(-1, 128)[:n].double()
+        want, e = torch.softmax(z, 0) @ V, torch.logsumexp(z, 0).item()
+        # as above; a lane's sum of weights is over the 16 rows' share of one warp's tiles (about
+        # n / (16 * 8 * 296)), the parts' sums are joined one after the other, at most 300 of them
+        terms = n / (16 * 8 * 296) + 300 + 16
+        err = 136 * 2.0 ** -23 * S
+        atol = (2 * err + 2.0 ** -15 + terms * 2.0 ** -22) * V.abs().max().item()
+        d = (outs[0][0][0, h].double() - want).abs()
+        assert (d <= 2.0 ** -8 * want.abs() + atol).all(), (h, d.max().item(), atol)
+        assert abs(outs[0][1][0, h].item() - e) <= err + terms * 2.0 ** -23 + 2.0 ** -21 + 2.0 ** -22 * abs(e)
+        del V, z
 
 
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
@@ -381,6 +439,12 @@ def test_decode_graph_and_two_streams():
         torch.cuda.synchronize()
         c.check(out, lse, lens=new)
         d.check(od, ld)
+    # a stream given by its address
+    out2, lse2 = c.outputs()
+    torch.cuda.synchronize()
+    rtp.rtp_paged_decode_step(c.desc, c.cache, c.q, lens, out2, lse2, c.ws, s.cuda_stream)
+    torch.cuda.synchronize()
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
     # another shape on the same workspace
     ws = d.ws
     e = Case(21, [700, 650], 16, "bf16", G=2, Hkv=4, ret=(True, False, True, False))
@@ -577,6 +641,7 @@ def _same(a, b):
 @pytest.mark.parametrize("inplace", [False, True])
 @pytest.mark.parametrize("B,page,stride,n_pages,n_new", [
     (1, 16, 1, 1, 1), (1, 16, 300, 301, 4800), (3, 64, 5, 11, 0), (33, 32, 7, 150, 9),
+    (64, 16, 300, 9000, 1), (600, 16, 40, 12000, 2), (5, 16, 3, 9, 4), (512, 32, 3, 900, 4),
     (513, 16, 9, 2500, 5), (4096, 16, 4, 9000, 3), (64, 256, 17, 700, 4097)])
 def test_reserve_random_rounds(B, page, stride, n_pages, n_new, inplace):
     """Rounds of starting, growing, shrinking and ending sequences, pages running out, the ring
@@ -593,6 +658,20 @@ def test_reserve_random_rounds(B, page, stride, n_pages, n_new, inplace):
         want = PO.reserve(page, n_pages, table, free, lens, new, counters, n_new)
         _same(_reserve(rtp, page, n_pages, table, free, lens, new, counters, n_new, inplace), want)
         table, free, lens, counters = want["table"], want["free"], want["lens"], want["counters"]
+
+
+def test_reserve_into_the_wished_lengths():
+    """lens_out may be new_lens."""
+    _, _, rtp = _mods()
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device=DEV)
+    lens, new, ctr = i32([0, 5, 40]), i32([33, 6, 0]), torch.tensor([0, 3], device=DEV)
+    table, free = i32([[9, 9, 9], [5, 9, 9], [3, 4, 6]]), i32([0, 1, 2, 9, 9, 9, 9])
+    slots, ws = i32([[0], [0], [0]]), torch.zeros(4096, dtype=torch.uint8, device=DEV)
+    rtp.rtp_paged_reserve(rtp.make_page_pool(free, table, 16), lens, new, ctr, new, ctr, slots, 1, ws)
+    assert new.tolist() == [33, 6, 0] and lens.tolist() == [0, 5, 40] and ctr.tolist() == [3, 6]
+    assert table.tolist() == [[0, 1, 2], [5, 9, 9], [3, 4, 6]]
+    assert free.tolist() == [0, 1, 2, 3, 4, 6, 9] and slots.tolist() == [[0], [85], [-1]]
+    assert rtp.rtp_read_device_status(ws) == 0 and rtp.rtp_last_launch_count() == 1
 
 
 def test_reserve_reports_bad_lengths_and_counters():

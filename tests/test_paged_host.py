@@ -241,6 +241,8 @@ def test_binding_builds_the_cache_struct():
     dict(v=torch.zeros((3, 2, 16, 128))),
     dict(k=torch.zeros((3, 16, 2, 128), dtype=torch.bfloat16).transpose(1, 2),
          v=torch.zeros((3, 16, 2, 128), dtype=torch.bfloat16).transpose(1, 2)),
+    dict(k=torch.zeros((1, 2, 16, 128), dtype=torch.bfloat16).expand(3, -1, -1, -1),
+         v=torch.zeros((1, 2, 16, 128), dtype=torch.bfloat16).expand(3, -1, -1, -1)),
     dict(block_table=torch.zeros((2, 4))), dict(block_table=torch.zeros(8, dtype=torch.int32)),
     dict(block_table=torch.zeros((4, 2), dtype=torch.int32).t()),
 ])
