@@ -1424,11 +1424,17 @@ paged_append_kernel(const __grid_constant__ PagedAppendParams P) {
   }
   cp_async_wait<0>();
   __syncthreads();
-  const int ln = tid & 15;
-  for (int it = tid >> 4; it < TOK * heads; it += 16) {
-    const int u = (int)((uint32_t)it * (last_y ? P.inv_last : 8192u) >> 16);
-    const int g = it - u * heads, slot = slots[u];
-    if (slot < 0) continue;
+  // half a warp stays with its token: 16 / TOK of them share out its heads
+  constexpr int kShare = 16 / TOK;
+  const int ln = tid & 15, u = (tid >> 4) / kShare;
+  slot = slots[u];
+  if (slot < 0) return;
+  double2 z4[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) z4[e] = ang[u][e][ln];
+  const int pid = slot >> P.C.lg;
+#pragma unroll 1
+  for (int g = (tid >> 4) % kShare; g < heads; g += kShare) {
     const unsigned char* kr = rows + (u * heads * 2 + g) * 256;
     const uint2 a = reinterpret_cast<const uint2*>(kr)[ln];
     const uint2 c = reinterpret_cast<const uint2*>(kr + 128)[ln];
@@ -1438,14 +1444,13 @@ paged_append_kernel(const __grid_constant__ PagedAppendParams P) {
     for (int e = 0; e < 4; ++e) {
       const uint32_t wa = e & 2 ? a.y : a.x, wc = e & 2 ? c.y : c.x;
       const double p = e & 1 ? bf_hi(wa) : bf_lo(wa), q = e & 1 ? bf_hi(wc) : bf_lo(wc);
-      const double2 z = ang[u][e][ln];
+      const double2 z = z4[e];
       kx[e] = p * z.x - q * z.y;
       kx[4 + e] = p * z.y + q * z.x;
     }
     float k[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) k[e] = (float)kx[e];
-    const int pid = slot >> P.C.lg;
     const int in = ((g0 + g) << P.C.lg) + (slot & ((1 << P.C.lg) - 1));
     const int64_t row = pid * P.C.page_stride + in;    // below 2^31
     if (KV == kKvBf16) {
