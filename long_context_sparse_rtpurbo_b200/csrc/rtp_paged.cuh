@@ -178,20 +178,30 @@ __device__ __forceinline__ float row_scale(float amax) {
   return fmaxf(__fdiv_rn(amax, kE4m3Max), kScaleMin);
 }
 
-// Four values as e4m3 bytes of x / scale, inv = 1 / scale rounded. The quotient in single
-// precision, rounded once: an estimate and Markstein's correction by its exact remainder. Where
-// the remainder could be too small a number for that, the values are divided.
-__device__ __forceinline__ uint32_t e4m3_of4(const float* x, float scale, float inv) {
-  float q[4];
+// Eight values as e4m3 bytes of x / scale, inv = 1 / scale rounded. The quotient in single
+// precision, rounded once: an estimate and Markstein's correction by its exact remainder, two
+// values an instruction. Where the remainder could be too small a number for that, the values are
+// divided.
+__device__ __forceinline__ uint2 e4m3_of8(const float* x, float scale, float inv) {
+  float q[8];
+  unsigned long long s2, i2;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(s2) : "f"(-scale));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(i2) : "f"(inv));
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    q[e] = x[e] * inv;
-    q[e] = fmaf(fmaf(-q[e], scale, x[e]), inv, q[e]);
+  for (int e = 0; e < 8; e += 2) {
+    unsigned long long x2, q2, r2;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x2) : "f"(x[e]), "f"(x[e + 1]));
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(q2) : "l"(x2), "l"(i2));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r2) : "l"(q2), "l"(s2), "l"(x2));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(q2) : "l"(r2), "l"(i2), "l"(q2));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(q[e]), "=f"(q[e + 1]) : "l"(q2));
   }
-  if (scale < 1e-25f || !(scale < 1e38f))
+  if (scale < 1e-25f || !(scale < 1e38f)) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) q[e] = __fdiv_rn(x[e], scale);
-  return f_e4m3x2(q[0], q[1]) | f_e4m3x2(q[2], q[3]) << 16;
+    for (int e = 0; e < 8; ++e) q[e] = __fdiv_rn(x[e], scale);
+  }
+  return make_uint2(f_e4m3x2(q[0], q[1]) | f_e4m3x2(q[2], q[3]) << 16,
+                    f_e4m3x2(q[4], q[5]) | f_e4m3x2(q[6], q[7]) << 16);
 }
 
 // ------------------------------------------------------------------ the line of tiles
@@ -1479,22 +1489,19 @@ paged_append_kernel(const __grid_constant__ PagedAppendParams P) {
       float mk = 0.f, mv = 0.f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) { mk = fmaxf(mk, fabsf(k[e])); mv = fmaxf(mv, fabsf(y[e])); }
+      // the first step of both maxima in one exchange: even lanes go on with the keys', odd lanes
+      // with the values', and divide for them
       const uint32_t team = 0xffffu << (tid & 16);
+      float top = fmaxf(ln & 1 ? mv : mk, __shfl_xor_sync(team, ln & 1 ? mk : mv, 1));
 #pragma unroll
-      for (int o = 1; o < 16; o <<= 1) {
-        mk = fmaxf(mk, __shfl_xor_sync(team, mk, o));
-        mv = fmaxf(mv, __shfl_xor_sync(team, mv, o));
-      }
-      // one division for both scales: even lanes the keys', odd lanes the values'
-      const float sc = row_scale(ln & 1 ? mv : mk), inv = __frcp_rn(sc);
+      for (int o = 2; o < 16; o <<= 1) top = fmaxf(top, __shfl_xor_sync(team, top, o));
+      const float sc = row_scale(top), inv = __frcp_rn(sc);
       const float sc2 = __shfl_xor_sync(team, sc, 1), inv2 = __shfl_xor_sync(team, inv, 1);
-      const float sk = ln & 1 ? sc2 : sc, ik = ln & 1 ? inv2 : inv;
-      const float sv = ln & 1 ? sc : sc2, iv = ln & 1 ? inv : inv2;
+      const uint2 k8 = e4m3_of8(k, ln & 1 ? sc2 : sc, ln & 1 ? inv2 : inv);
       unsigned char* kd = P.C.k + row * 128;
-      reinterpret_cast<uint32_t*>(kd)[ln] = e4m3_of4(k, sk, ik);
-      reinterpret_cast<uint32_t*>(kd + 64)[ln] = e4m3_of4(k + 4, sk, ik);
-      reinterpret_cast<uint2*>(P.C.v + row * 128)[ln] =
-          make_uint2(e4m3_of4(y, sv, iv), e4m3_of4(y + 4, sv, iv));
+      reinterpret_cast<uint32_t*>(kd)[ln] = k8.x;
+      reinterpret_cast<uint32_t*>(kd + 64)[ln] = k8.y;
+      reinterpret_cast<uint2*>(P.C.v + row * 128)[ln] = e4m3_of8(y, ln & 1 ? sc : sc2, ln & 1 ? inv : inv2);
       if (ln < 2) (ln ? P.C.vs : P.C.ks)[pid * ((int64_t)P.Hkv << P.C.lg) + in] = sc;
     }
   }
