@@ -595,8 +595,31 @@ int check_paged(const rtp_paged_cache* c, int Hkv, PagedPtrs& C) {
   return RTP_OK;
 }
 
+// A launch that may be set up while the one before it in the stream runs (its kernel begins with
+// launch_begin)
+template <class Params>
+int launch_overlapped(void (*kernel)(Params), dim3 grid, int threads, int smem, rtp_stream_t stream,
+                      const Params& P) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = (cudaStream_t)stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, P) != cudaSuccess) {
+    cudaGetLastError();                                // (not left behind for the caller's next check)
+    return RTP_ECUDA;
+  }
+  g_launches = 1;
+  return RTP_OK;
+}
+
 template <int KV, bool APPEND>
-int launch_paged(const PagedDecodeParams& P, const DevInfo& di, cudaStream_t st) {
+int launch_paged(const PagedDecodeParams& P, const DevInfo& di, rtp_stream_t stream) {
   constexpr int smem = PagedSmem<KV>::kBytes;
   const int rc = g_attr_paged.ensure(2 * KV + (APPEND ? 1 : 0), di.dev, smem, [](int, int bytes) {
     return cudaFuncSetAttribute(paged_decode_kernel<KV, APPEND>,
@@ -609,9 +632,7 @@ int launch_paged(const PagedDecodeParams& P, const DevInfo& di, cudaStream_t st)
   const int64_t most = (int64_t)P.L.B * P.L.Hkv * ((P.L.maxN + 15) / 16);
   const int64_t want = std::max<int64_t>((most + nw - 1) / nw, (int64_t)P.L.B * P.L.Hkv);
   const int grid = (int)std::min<int64_t>(std::min(di.sms, kPagedMaxCTAs), want);
-  paged_decode_kernel<KV, APPEND><<<grid, nw * 32, smem, st>>>(P);
-  g_launches = 1;
-  return cudaGetLastError() == cudaSuccess ? RTP_OK : RTP_ECUDA;
+  return launch_overlapped(paged_decode_kernel<KV, APPEND>, dim3(grid), nw * 32, smem, stream, P);
 }
 
 // rtp_paged_decode_step, with the decode token's append in the launch where append is set
@@ -641,10 +662,9 @@ int paged_decode_impl(const rtp_layer_desc* desc, const rtp_paged_cache* cache,
   P.part = at<float>(ws, kPagedCtrlBytes);
   P.head = P.part + (size_t)2 * kPagedMaxRanges * cta_part_floats(P.L.G);
   P.queue = at<uint32_t>(ws, 4 * kPagedQueue);
-  cudaStream_t st = (cudaStream_t)stream;
   if (cache->kv_type == RTP_KV_BF16)
-    return append ? launch_paged<kKvBf16, true>(P, di, st) : launch_paged<kKvBf16, false>(P, di, st);
-  return append ? launch_paged<kKvE4m3, true>(P, di, st) : launch_paged<kKvE4m3, false>(P, di, st);
+    return append ? launch_paged<kKvBf16, true>(P, di, stream) : launch_paged<kKvBf16, false>(P, di, stream);
+  return append ? launch_paged<kKvE4m3, true>(P, di, stream) : launch_paged<kKvE4m3, false>(P, di, stream);
 }
 
 }  // namespace
@@ -697,9 +717,7 @@ int rtp_paged_reserve(const rtp_page_pool* pool, const int32_t* lens, const int3
   int64_t ctas = P.B * ((pages + 31) / 32) / (2 * kResWarps);
   if (n_new > 0 && n_new <= kResLittle) ctas = P.B <= kResThreads ? 1 : P.B / 32;
   const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(di.sms, ctas));
-  paged_reserve_kernel<<<grid, kResThreads, 8 * (size_t)P.B, (cudaStream_t)stream>>>(P);
-  g_launches = 1;
-  return cudaGetLastError() == cudaSuccess ? RTP_OK : RTP_ECUDA;
+  return launch_overlapped(paged_reserve_kernel, dim3(grid), kResThreads, 8 * P.B, stream, P);
 }
 
 int rtp_paged_append_kv(const rtp_layer_desc* desc, const rtp_paged_cache* cache,
@@ -736,15 +754,12 @@ int rtp_paged_append_kv(const rtp_layer_desc* desc, const rtp_paged_cache* cache
   if (gx > 0x7fffffffLL) return RTP_ESHAPE;
   const dim3 grid((unsigned)gx, groups);
   const int smem = 4 * r * (1024 + heads * 512);       // at most 40 KB
-  cudaStream_t st = (cudaStream_t)stream;
   auto kernel = r == 1 ? paged_append_kernel<kKvBf16, 1>
                 : r == 2 ? paged_append_kernel<kKvBf16, 2> : paged_append_kernel<kKvBf16, 4>;
   if (cache->kv_type == RTP_KV_E4M3)
     kernel = r == 1 ? paged_append_kernel<kKvE4m3, 1>
              : r == 2 ? paged_append_kernel<kKvE4m3, 2> : paged_append_kernel<kKvE4m3, 4>;
-  kernel<<<grid, 256, smem, st>>>(P);
-  g_launches = 1;
-  return cudaGetLastError() == cudaSuccess ? RTP_OK : RTP_ECUDA;
+  return launch_overlapped(kernel, grid, 256, smem, stream, P);
 }
 
 int rtp_paged_decode_step(const rtp_layer_desc* desc, const rtp_paged_cache* cache,
