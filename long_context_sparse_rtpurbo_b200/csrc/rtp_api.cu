@@ -45,15 +45,18 @@ struct Plan {
       off_trace, total;
 };
 
-// theta_i = base^(-2i/d) and their sines: 192 library calls, so the last base's are kept per thread
-struct RopeTables { double base = 0.0, theta[kD / 2], cos1[kD / 2], sin1[kD / 2]; };
+// theta_i = base^(-2i/d), and (cos, sin) of 1, 2, 4 and 8 theta_i: library calls, so the last
+// base's are kept per thread
+struct RopeTables { double base = 0.0, theta[kD / 2]; double2 turn[4][kD / 2]; };
 const RopeTables& rope_tables(double base) {
   static thread_local RopeTables t;
   if (t.base != base) {
     for (int i = 0; i < kD / 2; ++i) {
       t.theta[i] = std::pow(base, -2.0 * i / (double)kD);
-      t.cos1[i] = std::cos(t.theta[i]);
-      t.sin1[i] = std::sin(t.theta[i]);
+      for (int k = 0; k < 4; ++k) {
+        const double x = t.theta[i] * (1 << k);
+        t.turn[k][i] = make_double2(std::cos(x), std::sin(x));
+      }
     }
     t.base = base;
   }
@@ -745,11 +748,12 @@ int rtp_paged_append_kv(const rtp_layer_desc* desc, const rtp_paged_cache* cache
   P.status = static_cast<int*>(ws);
   const RopeTables& rt = rope_tables(desc->rope_base);
   memcpy(P.theta, rt.theta, sizeof(P.theta));
-  memcpy(P.cos1, rt.cos1, sizeof(P.cos1));
-  memcpy(P.sin1, rt.sin1, sizeof(P.sin1));
   // short calls take a sine per token and angle, and more CTAs; long ones share it among
   // neighbouring tokens, the more the fewer rows a token has
   const int r = n_new < 16 ? 1 : heads <= 2 ? 4 : 2;
+  memcpy(P.turn[0], rt.turn[0], sizeof(P.turn[0]));
+  memcpy(P.turn[1], rt.turn[r >> 1], sizeof(P.turn[0]));          // r = 1, 2, 4
+  memcpy(P.turn[2], rt.turn[(r >> 1) + 1], sizeof(P.turn[0]));
   const int64_t gx = (P.n_tok + 4 * r - 1) / (4 * r);
   if (gx > 0x7fffffffLL) return RTP_ESHAPE;
   const dim3 grid((unsigned)gx, groups);
