@@ -396,7 +396,7 @@ struct TileDesc { int pid, row; uint32_t mask; };   // page, row in the page blo
 __device__ __forceinline__ TileDesc tile_desc(const PagedDecodeParams& P, const Cursor& c) {
   const int pos = 16 * (c.k < c.ns ? c.k : c.k + c.sh);
   TileDesc d;
-  d.pid = __ldg(c.pages + (pos >> P.C.lg));
+  d.pid = c.pages[pos >> P.C.lg];
   d.row = c.kvrow + (pos & ((1 << P.C.lg) - 1));
   d.mask = 0xffffu;
   if (pos + 16 > c.n || pos < c.lo)                    // the end, the window's edges
@@ -506,8 +506,8 @@ __device__ __forceinline__ void query_fetch(const PagedDecodeParams& P, QueryRaw
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int i = query_channel<KV>(kk, e);
-      R.lo[2 * kk + e] = __ldg(reinterpret_cast<const uint32_t*>(q + i));
-      R.hi[2 * kk + e] = __ldg(reinterpret_cast<const uint32_t*>(q + i + 64));
+      R.lo[2 * kk + e] = *reinterpret_cast<const uint32_t*>(q + i);
+      R.hi[2 * kk + e] = *reinterpret_cast<const uint32_t*>(q + i + 64);
     }
 }
 
@@ -1081,7 +1081,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams P) {
         const uint32_t mask = masks[slot];
         if (APPEND && cc.k == cc.nt - 1 && mask) {       // the last tile holds the new token's row
           const int pos = cc.n - 1;
-          const int pid = __ldg(P.C.table + (int64_t)cc.b * P.C.table_stride + (pos >> P.C.lg));
+          const int pid = P.C.table[(int64_t)cc.b * P.C.table_stride + (pos >> P.C.lg)];
           const int in = (kvh << P.C.lg) + (pos & ((1 << P.C.lg) - 1));
           paged_append_row<KV>(P, theta, cc.b, kvh, pos, pid * P.C.page_stride + in,
                                pid * (L.Hkv << P.C.lg) + in, stage);
