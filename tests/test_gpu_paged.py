@@ -821,3 +821,72 @@ def test_serving_step_in_one_graph():
                 c.agree(o[b, h], l[b, h], b, h, i + 1)
     assert t.lens.tolist() == [40] * B and t.counters.tolist() == [12, 40]
     assert t.status() == 0 and pl.status() == 0
+
+
+@pytest.mark.parametrize("kv", [torch.bfloat16, torch.float8_e4m3fn])
+@pytest.mark.parametrize("how", ["stream", "graph", "branches"])
+def test_launches_wait_for_those_before_them(how, kv):
+    """A run of reservations, appends and steps that each read what the launch before wrote, in
+    buffers that are overwritten between them by kernels, copies and fills: queued without a pause,
+    captured into a graph, and on two streams joined by events. The same bits as with the GPU
+    waited for after every call."""
+    _, layer, rtp = _mods()
+    rng = np.random.default_rng(62)
+    B, Hq, Hkv, page, cap, n, steps = 5, 8, 2, 16, 2048, 900, 24
+    qs, ks, vs = (_bf(rng.normal(size=(steps, B, h, 128))) for h in (Hq, Hkv, Hkv))
+    kp, vp = (_bf(rng.normal(size=(B, n, Hkv, 128))) for _ in range(2))
+    prompt = torch.tensor([900, 1, 0, 333, 64], dtype=torch.int32, device=DEV)
+    start = torch.zeros(B, dtype=torch.int32, device=DEV)
+
+    def run(pause, side=None, captured=False):
+        t = layer.PageTable(B, 400, page, cap)
+        pl = layer.PagedLayer(t, Hq, Hkv, 2, 100, cap, [1, 0], kv, BASE)
+        new, slots = torch.zeros_like(prompt), torch.zeros((B, n), dtype=torch.int32, device=DEV)
+        q, k, v = (torch.zeros_like(x[0]) for x in (qs, ks, vs))
+        out = torch.zeros_like(q)
+        outs = torch.zeros_like(qs)
+
+        def work():
+            rtp.rtp_paged_workspace_init(pl.ws)              # (a fill before a launch)
+            new.copy_(prompt)                                # (a copy before a launch)
+            t.reserve(new, slots); pause()
+            pl.append(kp, vp, start, slots); pause()
+            slots.fill_(-7)                                  # read by the launch before
+            for i in range(steps):
+                q.copy_(qs[i]); k.copy_(ks[i]); v.copy_(vs[i])
+                torch.add(t.lens, 1, out=new)
+                t.reserve(new); pause()
+                if side is None:
+                    pl.decode_append(k, v, q, t.lens, out); pause()
+                    outs[i].copy_(out)
+                else:                                        # the step on another stream
+                    main = torch.cuda.current_stream()
+                    side.wait_stream(main)
+                    with torch.cuda.stream(side):
+                        pl.decode_append(k, v, q, t.lens, out)
+                        outs[i].copy_(out)
+                    main.wait_stream(side)
+                out.zero_()
+
+        torch.cuda.synchronize()
+        if captured:
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                work()
+            for _ in range(2):                               # twice from the same start
+                t.lens.zero_()
+                t.counters.copy_(torch.tensor([0, 400]))
+                t.free_pages.copy_(torch.arange(400, dtype=torch.int32))
+                outs.zero_()
+                g.replay()
+        else:
+            work()
+        torch.cuda.synchronize()
+        assert t.status() == 0 and pl.status() == 0
+        return outs, t.lens.clone(), t.counters.clone()
+
+    run(torch.cuda.synchronize)                              # (loads every kernel)
+    want = run(torch.cuda.synchronize)
+    for captured in ([False, True] if how == "branches" else [how == "graph"]):
+        got = run(lambda: None, torch.cuda.Stream() if how == "branches" else None, captured)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
