@@ -222,7 +222,8 @@ int rtp_prefill(const rtp_layer_desc* desc, const uint16_t* q_pre, const uint16_
  * g * page_size + n % page_size of that page. All KV heads of a layer, local ones too, keep every
  * position (a local head reads its sinks and window only). A slot is page * page_size + row.
  * Entries of block_table behind a sequence's last page are not read. Several sequences may
- * share pages (a common prefix) as long as no call writes to a shared page.
+ * share pages (a common prefix) as long as no call writes to a shared page. Outputs overlap inputs
+ * only where a call says so.
  */
 enum {
   RTP_KV_BF16 = 0,      /* rows of 128 bf16 */
@@ -300,7 +301,7 @@ int rtp_paged_reserve(const rtp_page_pool* pool, const int32_t* lens, const int3
  *   k_pre, v  : bf16 [B][n_new][Hkv][128], pre-RoPE keys and values.
  *   start_pos : [B]; token j of sequence b is at position start_pos[b] + j.
  *   slot_map  : [B][n_new] slots, all different; a token with a negative slot is skipped.
- *   ws        : status word (may be NULL).
+ *   ws        : status word (4 bytes; may be NULL).
  * RTP_KV_BF16: the rows that rtp_append_kv writes, bit for bit (R(pos) k_pre evaluated in double
  * precision, rounded once; v). RTP_KV_E4M3: with x the row in single precision (the rotated key
  * rounded once), scale = max(max|x| / 448, 2^-126) and bytes x / scale, to nearest even.

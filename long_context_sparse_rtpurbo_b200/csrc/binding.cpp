@@ -141,6 +141,7 @@ PyObject* append_kv(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const auto* start = static_cast<const int32_t*>(data(a[7], "start_pos", kInt, B, dev));
     const auto* slots = static_cast<const int32_t*>(data(a[8], "slot_map", kInt, B * n_new, dev));
     const Space ws = workspace(a[10], dev);
+    if (ws.p && ws.bytes < 4) refuse("workspace: it does not hold the status word");
     const rtp_stream_t st = stream_of(a[11], dev);
     if (n_new != (int32_t)n_new) refuse("n_new is out of range");
     return unlocked([&] {

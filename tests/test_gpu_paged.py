@@ -890,3 +890,37 @@ def test_launches_wait_for_those_before_them(how, kv):
     for captured in ([False, True] if how == "branches" else [how == "graph"]):
         got = run(lambda: None, torch.cuda.Stream() if how == "branches" else None, captured)
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_append_e4m3_rows_of_extreme_size():
+    """Rows near both ends of the range, zeros, infinities and NaN at position 0 (where the rotation
+    changes no finite value): scale and bytes are those of the definition in single precision."""
+    _, _, rtp = _mods()
+    rng = np.random.default_rng(63)
+    B, Hkv, n, page = 1, 3, 64, 64
+    sizes = np.exp2(np.concatenate([np.arange(-133, -101), np.arange(96, 128)]))[:n]
+    with np.errstate(over="ignore"):
+        x = np.clip(rng.normal(size=(2, B, n, Hkv, 128)) * sizes[None, None, :, None, None],
+                    -3.3e38, 3.3e38)
+    x[:, 0, 5] = 0.0
+    x[1, 0, 6, 0, 3], x[1, 0, 6, 1, 127], x[1, 0, 7, 2, 64] = np.inf, -np.inf, np.nan
+    kv = [torch.from_numpy(a).to(DEV, torch.bfloat16) for a in x]
+    kv = [a.reshape(n, 1, Hkv, 128).contiguous() for a in kv]
+    k, v = (torch.zeros((1, Hkv, page, 128), dtype=torch.float8_e4m3fn, device=DEV) for _ in range(2))
+    ks, vs = (torch.zeros((1, Hkv, page), device=DEV) for _ in range(2))
+    desc = rtp.LayerDesc(n, Hkv, Hkv, 0, 1, 1 << 24, rtp.rtp_build_slot_map([1] * Hkv)[0], BASE)
+    cache = rtp.make_paged_cache(k, v, torch.zeros((n, 1), dtype=torch.int32, device=DEV), ks, vs)
+    ws = torch.zeros(4096, dtype=torch.uint8, device=DEV)
+    slots = torch.arange(n, dtype=torch.int32, device=DEV).reshape(n, 1)
+    rtp.rtp_paged_append_kv(desc, cache, kv[0], kv[1], torch.zeros(n, dtype=torch.int32, device=DEV), slots,
+                            1, ws)  # each token the first of a sequence
+    assert rtp.rtp_read_device_status(ws) == 0
+    for rows, got, sc in ((kv[0], k, ks), (kv[1], v, vs)):
+        w = rows[:, 0].float().cpu().numpy().swapaxes(0, 1)        # [Hkv][n][128]
+        amax = np.fmax.reduce(np.abs(w), axis=-1, initial=0.0).astype(np.float32)
+        scale = np.maximum(amax / np.float32(448), np.float32(2.0 ** -126))
+        assert np.array_equal(sc[0].cpu().numpy(), scale)
+        with np.errstate(invalid="ignore"):
+            q = w / scale[..., None]
+        want = np.where(np.isnan(q), np.nan, PO.e4m3_round(np.nan_to_num(q.astype(np.float64))))
+        assert np.array_equal(got[0].float().cpu().numpy(), want, equal_nan=True)

@@ -280,3 +280,16 @@ def test_binding_refuses_bad_arguments():
         args[a[0]] = torch.zeros(2)
         with pytest.raises(ValueError):
             rtp.rtp_paged_reserve(pool, *args, i32(2, 1), 1, torch.zeros(4096, dtype=torch.uint8))
+
+
+def test_append_refuses_a_workspace_without_a_status_word():
+    lib, c = _lib.load(), _cache()
+    d = _desc()
+    assert lib.rtp_paged_append_kv(d.ref, ctypes.byref(c), X, X, X, X, 4, X + 2, None) == _lib.RTP_EWORKSPACE
+    c = _cpu_cache()
+    d = rtp.LayerDesc(2, 4, 2, 4, 64, 64, rtp.rtp_build_slot_map([1, 0])[0])
+    rows = torch.zeros((2, 3, 2, 128), dtype=torch.bfloat16)
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)
+    with pytest.raises(ValueError, match="status word"):
+        rtp.rtp_paged_append_kv(d, c, rows, rows, i32(2), i32(2, 3), 3,
+                                torch.zeros(3, dtype=torch.uint8))
