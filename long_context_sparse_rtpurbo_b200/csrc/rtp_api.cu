@@ -45,15 +45,15 @@ struct Plan {
       off_trace, total;
 };
 
-// theta_i = base^(-2i/d), and (cos, sin) of 1, 2, 4 and 8 theta_i: library calls, so the last
+// theta_i = base^(-2i/d), and (cos, sin) of 1, 2 and 4 theta_i: library calls, so the last
 // base's are kept per thread
-struct RopeTables { double base = 0.0, theta[kD / 2]; double2 turn[4][kD / 2]; };
+struct RopeTables { double base = 0.0, theta[kD / 2]; double2 turn[3][kD / 2]; };
 const RopeTables& rope_tables(double base) {
   static thread_local RopeTables t;
   if (t.base != base) {
     for (int i = 0; i < kD / 2; ++i) {
       t.theta[i] = std::pow(base, -2.0 * i / (double)kD);
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < 3; ++k) {
         const double x = t.theta[i] * (1 << k);
         t.turn[k][i] = make_double2(std::cos(x), std::sin(x));
       }
@@ -754,17 +754,17 @@ int rtp_paged_append_kv(const rtp_layer_desc* desc, const rtp_paged_cache* cache
   const int r = n_new < 16 ? 1 : heads <= 2 ? 4 : 2;
   memcpy(P.turn[0], rt.turn[0], sizeof(P.turn[0]));
   memcpy(P.turn[1], rt.turn[r >> 1], sizeof(P.turn[0]));          // r = 1, 2, 4
-  memcpy(P.turn[2], rt.turn[(r >> 1) + 1], sizeof(P.turn[0]));
-  const int64_t gx = (P.n_tok + 4 * r - 1) / (4 * r);
+  const int tok = kAppendThreads / 64 * r;
+  const int64_t gx = (P.n_tok + tok - 1) / tok;
   if (gx > 0x7fffffffLL) return RTP_ESHAPE;
   const dim3 grid((unsigned)gx, groups);
-  const int smem = 4 * r * (1024 + heads * 512);       // at most 40 KB
+  const int smem = tok * (1024 + heads * 512);         // at most 20 KB
   auto kernel = r == 1 ? paged_append_kernel<kKvBf16, 1>
                 : r == 2 ? paged_append_kernel<kKvBf16, 2> : paged_append_kernel<kKvBf16, 4>;
   if (cache->kv_type == RTP_KV_E4M3)
     kernel = r == 1 ? paged_append_kernel<kKvE4m3, 1>
              : r == 2 ? paged_append_kernel<kKvE4m3, 2> : paged_append_kernel<kKvE4m3, 4>;
-  return launch_overlapped(kernel, grid, 256, smem, stream, P);
+  return launch_overlapped(kernel, grid, kAppendThreads, smem, stream, P);
 }
 
 int rtp_paged_decode_step(const rtp_layer_desc* desc, const rtp_paged_cache* cache,

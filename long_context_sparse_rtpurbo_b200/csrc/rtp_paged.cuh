@@ -1362,26 +1362,27 @@ struct PagedAppendParams {
   int64_t n_tok, cap_rows;       // B * n_new; n_pages * page
   int n_new, Hkv;
   uint32_t inv_last;             // 2^16 / (heads of the last block of 8) rounded up: divides exactly
-  int step_last;                 // tokens that 256 threads copy at once in the last block
+  int step_last;                 // tokens that a CTA copies at once in the last block
   int* status;
   double theta[kD / 2];          // theta_i
-  double2 turn[3][kD / 2];       // (cos, sin) of theta_i, of R theta_i and of 2 R theta_i
+  double2 turn[2][kD / 2];       // (cos, sin) of theta_i and of R theta_i
 };
 
-// A CTA of 256 threads takes up to 8 KV heads of 4 R consecutive tokens of the flattened
+// A CTA of 128 threads takes up to 8 KV heads of 2 R consecutive tokens of the flattened
 // [B][n_new] axis. Their rows, contiguous in the inputs, are copied to shared memory while the
 // angles are made, once for all heads: sin and cos in double of the first token's 64 angles, the
 // other tokens of its sequence by turning on (products of cos and sin of theta). Then half a warp
-// per (token, KV head) row, 4 channel pairs a lane, in double.
+// per (token, KV head) row, 4 channel pairs a lane, in double. (Eight CTAs an SM, each at another
+// of these stages; 256 threads and twice the tokens were 2 to 7 % slower.)
 // Bound by HBM: 512 B read, 512 (264) B written per row; bf16 rows run at it (32K tokens of 8 KV
-// heads in 44 us, 6.1 TB/s), e4m3 rows at the issue of instructions (54 us; 300 a row pair, 193
+// heads in 43 us, 6.2 TB/s), e4m3 rows at the issue of instructions (51 us; 300 a row pair, 193
 // for bf16). Single precision with carried errors took twice the instructions.
-constexpr int kAppendHeads = 8;
+constexpr int kAppendHeads = 8, kAppendThreads = 128;
 
 template <int KV, int R>
-__global__ void __launch_bounds__(256, 4)
+__global__ void __launch_bounds__(kAppendThreads, 8)
 paged_append_kernel(const __grid_constant__ PagedAppendParams P) {
-  constexpr int TOK = 4 * R;
+  constexpr int TOK = 2 * R;
   // (cos, sin) as the lanes read them: [token][channel % 4][channel / 4]; the tokens' K and V rows
   extern __shared__ __align__(16) unsigned char asm_[];
   double2(*ang)[4][16] = reinterpret_cast<double2(*)[4][16]>(asm_);
@@ -1389,7 +1390,7 @@ paged_append_kernel(const __grid_constant__ PagedAppendParams P) {
   __shared__ int32_t slots[TOK];
   const int tid = threadIdx.x, i = tid & 63, sub = tid >> 6;
   const double th = ld_gen(&P.theta[i]);
-  const double2 z1 = ld_gen(&P.turn[0][i]), zr = ld_gen(&P.turn[1][i]), z2r = ld_gen(&P.turn[2][i]);
+  const double2 z1 = ld_gen(&P.turn[0][i]), zr = ld_gen(&P.turn[1][i]);
   launch_begin();
   const int64_t tok0 = (int64_t)blockIdx.x * TOK;
   const int g0 = blockIdx.y * kAppendHeads, heads = min(P.Hkv - g0, kAppendHeads);
@@ -1399,18 +1400,19 @@ paged_append_kernel(const __grid_constant__ PagedAppendParams P) {
   if (tid < TOK) slots[tid] = slot;
   if (!__syncthreads_or(slot >= 0)) return;            // a CTA of padding
   {
-    // a token's K and V are 32 * heads pieces of 16 bytes; a pass covers as many whole tokens as
-    // there are threads for
-    const int per = heads * 32, u0 = (int)((uint32_t)(tid >> 5) * (last_y ? P.inv_last : 8192u) >> 16);
-    const int x = tid - u0 * per, step = last_y ? P.step_last : 1;
-    const bool isk = x < heads * 16;
-    const uint16_t* src = (isk ? P.k_pre : P.v) + ((tok0 + u0) * P.Hkv + g0) * kD +
-                          (isk ? x : x - heads * 16) * 8;
+    // a token's K are 16 * heads pieces of 16 bytes, and its V; a pass covers as many whole tokens
+    // as there are threads for
+    const int u0 = (int)((uint32_t)(tid >> 4) * (last_y ? P.inv_last : 8192u) >> 16);
+    const int x = tid - u0 * heads * 16, step = last_y ? P.step_last : 1;
+    int64_t src = ((tok0 + u0) * P.Hkv + g0) * kD + x * 8;
     if (u0 < step) {
-      uint32_t dst = smem_u32(rows) + tid * 16;
+      uint32_t dst = smem_u32(rows) + u0 * heads * 512 + x * 16;
 #pragma unroll 4
-      for (int u = u0; u < TOK; u += step, src += (int64_t)step * P.Hkv * kD, dst += step * per * 16)
-        if (slots[u] >= 0) cp_async16_s(dst, src);
+      for (int u = u0; u < TOK; u += step, src += step * P.Hkv * kD, dst += step * heads * 512)
+        if (slots[u] >= 0) {
+          cp_async16_s(dst, P.k_pre + src);
+          cp_async16_s(dst + heads * 256, P.v + src);
+        }
     }
     cp_async_commit();
   }
@@ -1426,8 +1428,7 @@ paged_append_kernel(const __grid_constant__ PagedAppendParams P) {
     __syncthreads();
     if (turn) {
       z = ang[0][i & 3][i >> 2];
-      if (sub & 1) z = turned(z, zr);
-      if (sub & 2) z = turned(z, z2r);
+      z = turned(z, zr);
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -1452,8 +1453,8 @@ paged_append_kernel(const __grid_constant__ PagedAppendParams P) {
   }
   cp_async_wait<0>();
   __syncthreads();
-  // half a warp stays with its token: 16 / TOK of them share out its heads
-  constexpr int kShare = 16 / TOK;
+  // half a warp stays with its token: 8 / TOK of them share out its heads
+  constexpr int kShare = 8 / TOK;
   const int ln = tid & 15, u = (tid >> 4) / kShare;
   slot = slots[u];
   if (slot < 0) return;
