@@ -749,9 +749,14 @@ int rtp_paged_append_kv(const rtp_layer_desc* desc, const rtp_paged_cache* cache
   P.status = static_cast<int*>(ws);
   const RopeTables& rt = rope_tables(desc->rope_base);
   memcpy(P.theta, rt.theta, sizeof(P.theta));
-  // short calls take a sine per token and angle, and more CTAs; long ones share it among
-  // neighbouring tokens, the more the fewer rows a token has
-  const int r = n_new < 16 ? 1 : heads <= 2 ? 4 : 2;
+  // R = 2 or 4 (for few rows a token) shares a sine among neighbouring tokens: 32K tokens of 8 KV
+  // heads take 50, 43 and 46 us with R = 1, 2 and 4, of 4 heads 37, 27 and 24. Calls of fewer than
+  // five such CTAs an SM, or of few tokens a sequence, take more CTAs instead: 64 x 24 tokens 3.9
+  // us with R = 1, 4.6 with 2.
+  DevInfo di;
+  if (dev_info(di) != RTP_OK) return RTP_ECUDA;
+  int r = n_new < 16 ? 1 : heads <= 4 ? 4 : 2;
+  while (r > 1 && P.n_tok * groups / (kAppendThreads / 64 * r) < 5 * di.sms) r >>= 1;
   memcpy(P.turn[0], rt.turn[0], sizeof(P.turn[0]));
   memcpy(P.turn[1], rt.turn[r >> 1], sizeof(P.turn[0]));          // r = 1, 2, 4
   const int tok = kAppendThreads / 64 * r;

@@ -924,3 +924,45 @@ def test_append_e4m3_rows_of_extreme_size():
             q = w / scale[..., None]
         want = np.where(np.isnan(q), np.nan, PO.e4m3_round(np.nan_to_num(q.astype(np.float64))))
         assert np.array_equal(got[0].float().cpu().numpy(), want, equal_nan=True)
+
+
+@pytest.mark.parametrize("Hkv", [1, 3, 4, 5, 8, 9, 13])
+@pytest.mark.parametrize("B,n_new", [(7, 16), (3, 701), (5, 1003), (9, 801)])
+def test_append_is_the_same_however_it_is_cut(Hkv, B, n_new):
+    """Calls of sizes that share a sine among one, two or four tokens, whose blocks of tokens end
+    inside a sequence and cross into the next, against the formula in 64 bits: turning
+    an angle on by products in double moves it by less than 2^-48, so all but roundings within that
+    of a border are the same."""
+    _, _, rtp = _mods()
+    rng = np.random.default_rng(Hkv * 1000 + n_new)
+    page, start = 64, 1000
+    per = -(-n_new // page)
+    ids = rng.permutation(B * per)
+    j = np.arange(n_new)
+    slots = np.stack([ids[b * per + j // page] * page + j % page for b in range(B)])
+    slots[0, 3] = -1
+    kp, vp = (_bf(rng.normal(size=(B, n_new, Hkv, 128))) for _ in range(2))
+    k, v = (torch.full((B * per, Hkv, page, 128), 7.0, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    ret = [1] * Hkv
+    desc = rtp.LayerDesc(B, Hkv, Hkv, 0, 1, 1 << 24, rtp.rtp_build_slot_map(ret)[0], BASE)
+    cache = rtp.make_paged_cache(k, v, torch.zeros((B, 1), dtype=torch.int32, device=DEV))
+    pos = torch.full((B,), start, dtype=torch.int32, device=DEV)
+    rtp.rtp_paged_append_kv(desc, cache, kp, vp, pos, torch.from_numpy(slots.astype(np.int32)).to(DEV), n_new)
+    th = BASE ** (-np.arange(64) / 64.0)
+    a = (start + j)[:, None, None] * th
+    x = kp.double().cpu().numpy()
+    want = np.concatenate([x[..., :64] * np.cos(a) - x[..., 64:] * np.sin(a),
+                           x[..., :64] * np.sin(a) + x[..., 64:] * np.cos(a)], -1)
+    got_k, got_v = k.float().cpu().numpy(), v.float().cpu().numpy()
+    for b in range(B):
+        keep = slots[b] >= 0
+        pg, r = slots[b, keep] // page, slots[b, keep] % page
+        gk = got_k[pg, :, r]
+        bad = gk != bf16_round(want[b, keep])
+        assert bad.sum() <= 1e-6 * bad.size + 1
+        # half a bf16 step, and the angles' error on either side
+        assert (np.abs(gk - want[b, keep]) <= 2.0 ** -8 * np.abs(want[b, keep]) + 2.0 ** -40).all()
+        assert np.array_equal(got_v[pg, :, r], vp[b].float().cpu().numpy()[keep])
+    touched = np.zeros((B * per, page), bool)
+    touched.reshape(-1)[slots[slots >= 0]] = True
+    assert (got_k.swapaxes(1, 2)[~touched] == 7.0).all() and (got_v.swapaxes(1, 2)[~touched] == 7.0).all()
