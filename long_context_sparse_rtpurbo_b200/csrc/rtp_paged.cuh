@@ -921,7 +921,11 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams P) {
   if (tid < 2 * NW) ent[tid].gid = -1;
   bool bad = false;
   if (nc == 1) lens = paged_len(P, lane, &bad);
-  if (lane == 0) {                                     // while the lengths are on their way
+  // while the lengths are on their way (the short way, 0.3 us less of 11, made the registers of the
+  // e4m3 kernel come out 3 % slower on long lines)
+  if (KV == kKvBf16) {
+    if (tid < kD / 2) theta[tid] = ld_gen(&L.theta[tid]);
+  } else if (lane == 0) {
 #pragma unroll
     for (int i = 0; i < (kD / 2 + NW - 1) / NW; ++i)
       if (warp + i * NW < kD / 2) theta[warp + i * NW] = L.theta[warp + i * NW];
