@@ -763,7 +763,7 @@ int rtp_paged_append_kv(const rtp_layer_desc* desc, const rtp_paged_cache* cache
   const int64_t gx = (P.n_tok + tok - 1) / tok;
   if (gx > 0x7fffffffLL) return RTP_ESHAPE;
   const dim3 grid((unsigned)gx, groups);
-  const int smem = tok * (1024 + heads * 512);         // at most 20 KB
+  const int smem = tok * (1024 + heads * 512);         // at most 24 KB
   auto kernel = r == 1 ? paged_append_kernel<kKvBf16, 1>
                 : r == 2 ? paged_append_kernel<kKvBf16, 2> : paged_append_kernel<kKvBf16, 4>;
   if (cache->kv_type == RTP_KV_E4M3)
