@@ -289,12 +289,25 @@ int rtp_paged_workspace_init(void* ws, size_t ws_bytes, rtp_stream_t stream);
  * lens_out and counters_out may be lens (or new_lens) and counters themselves.
  * A length outside [0, table_stride * page_size] leaves that sequence as it is, and counters or
  * lengths that cannot be this pool's (more free and returned pages than n_pages) leave all as
- * they are; both set RTP_EDEVICE in ws's status word. Running out of pages is no error.
+ * they are; both set RTP_EDEVICE in ws's status word. Running out of pages is no error: what
+ * writes or reads the new tokens next has to leave the sequences out that were not served. Their
+ * slots are -1, and rtp_paged_reserve_step gives the lengths of such a step.
  */
 int rtp_paged_reserve(const rtp_page_pool* pool, const int32_t* lens, const int32_t* new_lens,
                       const int64_t* counters, int32_t* lens_out, int64_t* counters_out,
                       int32_t* slot_map, int32_t n_new, void* ws, size_t ws_bytes,
                       rtp_stream_t stream);
+
+/*
+ * rtp_paged_reserve that also writes the seq_lens of the decode step it was made for:
+ *   step_lens : [B] new_lens[b] where the sequence was served and grew, 0 elsewhere (an idle place:
+ *               no token, ended, or no pages left for it). Overlaps no other argument. NULL: not
+ *               written.
+ */
+int rtp_paged_reserve_step(const rtp_page_pool* pool, const int32_t* lens, const int32_t* new_lens,
+                           const int64_t* counters, int32_t* lens_out, int64_t* counters_out,
+                           int32_t* slot_map, int32_t n_new, int32_t* step_lens, void* ws,
+                           size_t ws_bytes, rtp_stream_t stream);
 
 /*
  * Writes new tokens to their slots (one launch).
@@ -334,6 +347,9 @@ int rtp_paged_decode_step(const rtp_layer_desc* desc, const rtp_paged_cache* cac
  * rtp_paged_append_kv of the decode token (position seq_lens[b] - 1, slot by the block table)
  * and rtp_paged_decode_step in one launch, with the same results.
  *   k_new, v_new : bf16 [B][Hkv][128]. The page of the token must not be shared.
+ * seq_lens counts the new token: every sequence of a length n > 0 gets its row n - 1 written. A
+ * sequence that the reservation did not serve keeps its length, which would put the token over its
+ * last row: give the step_lens of rtp_paged_reserve_step, where it is an idle place.
  */
 int rtp_paged_decode_step_append(const rtp_layer_desc* desc, const rtp_paged_cache* cache,
                                  const uint16_t* k_new, const uint16_t* v_new,
@@ -387,10 +403,9 @@ int32_t rtp_last_launch_count(void);
  *     undefined and its workspace must be re-initialised with rtp_workspace_init. Process-wide.
  *   rtp_debug_fail_next_call: the next call of rtp_append_kv, rtp_decode_step,
  *     rtp_decode_step_append, rtp_decode_step_topk, rtp_decode_step_static, rtp_prefill or of a
- *     paged entry point (rtp_paged_reserve, _append_kv, _decode_step, _decode_step_append), on
- *     any thread, returns `status` (one
- *     of the negative RTP_E* codes; 0 cancels) before checking its arguments, and enqueues
- *     nothing. Process-wide, consumed by that one call.
+ *     paged entry point (rtp_paged_reserve, _reserve_step, _append_kv, _decode_step,
+ *     _decode_step_append), on any thread, returns `status` (one of the negative RTP_E* codes; 0
+ *     cancels) before checking its arguments, and enqueues nothing. Process-wide, consumed by that one call.
  */
 int rtp_debug_set_wait_limit(int64_t cycles);
 int rtp_debug_fail_next_call(int status);

@@ -17,7 +17,7 @@ EXPORTS = (
     "rtp_decode_step_static", "rtp_decode_step_append", "rtp_decode_step_topk", "rtp_debug_set_wait_limit",
     "rtp_debug_fail_next_call", "rtp_prefill_workspace_bytes", "rtp_prefill",
     "rtp_paged_workspace_bytes", "rtp_paged_workspace_init", "rtp_paged_reserve",
-    "rtp_paged_append_kv", "rtp_paged_decode_step", "rtp_paged_decode_step_append",
+    "rtp_paged_reserve_step", "rtp_paged_append_kv", "rtp_paged_decode_step", "rtp_paged_decode_step_append",
 )
 RTP_STATIC_SCRATCH_BYTES = 16 << 20
 RTP_KV_BF16, RTP_KV_E4M3 = 0, 1
@@ -75,7 +75,7 @@ def native():
         except ImportError as e:
             raise RuntimeError("_binding.so is not built; run __graft_entry__.build() first") from e
         _binding.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
-            lib.rtp_paged_reserve, lib.rtp_paged_append_kv, lib.rtp_paged_decode_step,
+            lib.rtp_paged_reserve_step, lib.rtp_paged_append_kv, lib.rtp_paged_decode_step,
             lib.rtp_paged_decode_step_append)))
         _native = _binding
     return _native
@@ -122,6 +122,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.rtp_paged_workspace_init.argtypes = [vp, sz, vp]
     lib.rtp_paged_reserve.restype = ctypes.c_int
     lib.rtp_paged_reserve.argtypes = [PP, vp, vp, vp, vp, vp, vp, i32, vp, sz, vp]
+    lib.rtp_paged_reserve_step.restype = ctypes.c_int
+    lib.rtp_paged_reserve_step.argtypes = [PP, vp, vp, vp, vp, vp, vp, i32, vp, vp, sz, vp]
     lib.rtp_paged_append_kv.restype = ctypes.c_int
     lib.rtp_paged_append_kv.argtypes = [D, PC, vp, vp, vp, vp, i32, vp, vp]
     lib.rtp_paged_decode_step.restype = ctypes.c_int

@@ -15,7 +15,7 @@
 
 namespace {
 
-decltype(&rtp_paged_reserve) f_reserve;
+decltype(&rtp_paged_reserve_step) f_reserve;
 decltype(&rtp_paged_append_kv) f_append;
 decltype(&rtp_paged_decode_step) f_decode;
 decltype(&rtp_paged_decode_step_append) f_decode_append;
@@ -109,9 +109,10 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// (pool, B, device, lens, new_lens, counters, lens_out, counters_out, slot_map, n_new, ws, stream)
+// (pool, B, device, lens, new_lens, counters, lens_out, counters_out, slot_map, n_new, step_lens, ws,
+// stream); step_lens may be None
 PyObject* reserve(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 12, [&] {
+  return guarded(n, 13, [&] {
     const auto* pool = address<const rtp_page_pool>(a[0]);
     const int64_t B = number(a[1]), dev = number(a[2]), n_new = number(a[9]);
     const auto* lens = static_cast<const int32_t*>(data(a[3], "lens", kInt, B, dev));
@@ -120,11 +121,13 @@ PyObject* reserve(PyObject*, PyObject* const* a, Py_ssize_t n) {
     auto* lens_out = static_cast<int32_t*>(data(a[6], "lens_out", kInt, B, dev));
     auto* ctr_out = static_cast<int64_t*>(data(a[7], "counters_out", kLong, 2, dev));
     auto* slots = static_cast<int32_t*>(data(a[8], "slot_map", kInt, B * n_new, dev, n_new == 0));
-    const Space ws = workspace(a[10], dev);
-    const rtp_stream_t st = stream_of(a[11], dev);
+    auto* step = static_cast<int32_t*>(data(a[10], "step_lens", kInt, B, dev, true));
+    const Space ws = workspace(a[11], dev);
+    const rtp_stream_t st = stream_of(a[12], dev);
     if (n_new != (int32_t)n_new) refuse("n_new is out of range");
     return unlocked([&] {
-      return f_reserve(pool, lens, wish, ctr, lens_out, ctr_out, slots, (int32_t)n_new, ws.p, ws.bytes, st);
+      return f_reserve(pool, lens, wish, ctr, lens_out, ctr_out, slots, (int32_t)n_new, step, ws.p, ws.bytes,
+                       st);
     });
   });
 }

@@ -692,6 +692,14 @@ int rtp_paged_reserve(const rtp_page_pool* pool, const int32_t* lens, const int3
                       const int64_t* counters, int32_t* lens_out, int64_t* counters_out,
                       int32_t* slot_map, int32_t n_new, void* ws, size_t ws_bytes,
                       rtp_stream_t stream) {
+  return rtp_paged_reserve_step(pool, lens, new_lens, counters, lens_out, counters_out, slot_map, n_new,
+                                nullptr, ws, ws_bytes, stream);
+}
+
+int rtp_paged_reserve_step(const rtp_page_pool* pool, const int32_t* lens, const int32_t* new_lens,
+                           const int64_t* counters, int32_t* lens_out, int64_t* counters_out,
+                           int32_t* slot_map, int32_t n_new, int32_t* step_lens, void* ws,
+                           size_t ws_bytes, rtp_stream_t stream) {
   g_launches = 0;
   if (const int inj = take_injected()) return inj;
   if (!pool || !pool->free_pages || !pool->block_table || !lens || !new_lens || !counters ||
@@ -707,7 +715,7 @@ int rtp_paged_reserve(const rtp_page_pool* pool, const int32_t* lens, const int3
   if (dev_info(di) != RTP_OK) return RTP_ECUDA;
   PagedReserveParams P;
   P.free_pages = pool->free_pages; P.table = pool->block_table; P.slot_map = slot_map;
-  P.lens_out = lens_out; P.lens = lens; P.new_lens = new_lens;
+  P.lens_out = lens_out; P.step_lens = step_lens; P.lens = lens; P.new_lens = new_lens;
   P.counters = counters; P.counters_out = counters_out;
   P.cap = std::min<int64_t>((int64_t)pool->table_stride << lg, 0x7fffffffLL);
   P.B = pool->B; P.n_new = n_new; P.n_pages = pool->n_pages; P.stride = pool->table_stride;

@@ -1533,7 +1533,7 @@ paged_append_kernel(const __grid_constant__ PagedAppendParams P) {
 // ------------------------------------------------------------------ page reservation
 
 struct PagedReserveParams {
-  int32_t *free_pages, *table, *slot_map, *lens_out;
+  int32_t *free_pages, *table, *slot_map, *lens_out, *step_lens;
   const int32_t *lens, *new_lens;
   const int64_t* counters;
   int64_t* counters_out;
@@ -1758,7 +1758,11 @@ paged_reserve_kernel(const __grid_constant__ PagedReserveParams P) {
   if (!s_last) return;
 #pragma unroll
   for (int k = 0; k < kResPer; ++k)
-    if (k < per && first + k < P.B) P.lens_out[first + k] = (served >> k) & 1u ? n1[k] : n0[k];
+    if (k < per && first + k < P.B) {
+      const bool got = (served >> k) & 1u;
+      P.lens_out[first + k] = got ? n1[k] : n0[k];
+      if (P.step_lens) P.step_lens[first + k] = got && n1[k] > n0[k] ? n1[k] : 0;
+    }
   if (tid == 0) {
     P.counters_out[0] = ok ? head + s_taken : head;
     P.counters_out[1] = ok ? tail + run_c : tail;

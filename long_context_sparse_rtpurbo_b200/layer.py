@@ -106,6 +106,7 @@ class PageTable:
         i32 = dict(dtype=torch.int32, device=device)
         self.B, self.n_pages, self.page_size = B, n_pages, page_size
         self.lens = torch.zeros(B, **i32)
+        self.step_lens = torch.zeros(B, **i32)
         self.block_table = torch.zeros((B, max(1, -(-max_seq_len // page_size))), **i32)
         self.free_pages = torch.arange(n_pages, **i32)
         self.counters = torch.tensor([0, n_pages], dtype=torch.int64, device=device)
@@ -116,10 +117,13 @@ class PageTable:
     def reserve(self, new_lens, slot_map=None, stream=None):
         """Takes or returns pages so that sequence b holds new_lens[b] tokens (int32 [B]; 0 ends
         it) and writes the slots of its new tokens to slot_map (int32 [B][n_new]). Updates lens
-        in place: a sequence that the free pages do not suffice for keeps its length."""
+        in place: a sequence that the free pages do not suffice for keeps its length. step_lens
+        then holds the lengths of the sequences that grew and 0 for the others: the seq_lens of
+        the decode step over the new tokens."""
         n_new = 0 if slot_map is None else slot_map.shape[1]
-        return rtp.rtp_paged_reserve(self.pool, self.lens, new_lens, self.counters, self.lens,
-                                     self.counters, slot_map, n_new, self.ws, stream)
+        return rtp.rtp_paged_reserve_step(self.pool, self.lens, new_lens, self.counters, self.lens,
+                                          self.counters, slot_map, n_new, self.step_lens, self.ws,
+                                          stream)
 
     def status(self, stream=None) -> int:
         return rtp.rtp_read_device_status(self.ws, stream)
@@ -159,12 +163,15 @@ class PagedLayer:
                                        k_pre.shape[1], self.ws, stream)
 
     def decode(self, q_pre, seq_lens, out, lse=None, stream=None):
+        """Decode step at position seq_lens - 1, whose token the pages hold (0: an idle place)."""
         return rtp.rtp_paged_decode_step(self.desc, self.cache, q_pre, seq_lens, out, lse, self.ws,
                                          stream)
 
     def decode_append(self, k_new, v_new, q_pre, seq_lens, out, lse=None, stream=None):
         """Append of the decode token (k_new, v_new: bf16 [B][Hkv][128] at seq_lens - 1, whose
-        page is reserved) and the decode step in one launch."""
+        page is reserved) and the decode step in one launch. After a reservation seq_lens is the
+        table's step_lens: under its lens, a sequence that got no page would have its last row
+        overwritten."""
         return rtp.rtp_paged_decode_step_append(self.desc, self.cache, k_new, v_new, q_pre,
                                                 seq_lens, out, lse, self.ws, stream)
 

@@ -245,7 +245,16 @@ def rtp_paged_reserve(pool: PagePoolRef, lens, new_lens, counters, lens_out, cou
     int32 [B]; counters, counters_out: int64 [2]; slot_map: int32 [B][n_new]."""
     return _check("rtp_paged_reserve", (_lib._native or _lib.native()).reserve(
         pool.addr, pool.B, pool.device_index, lens, new_lens, counters, lens_out, counters_out,
-        slot_map, n_new, ws, _stream_arg(stream)))
+        slot_map, n_new, None, ws, _stream_arg(stream)))
+
+
+def rtp_paged_reserve_step(pool: PagePoolRef, lens, new_lens, counters, lens_out, counters_out,
+                           slot_map, n_new, step_lens, ws, stream=None):
+    """rtp_paged_reserve that also writes the decode step's lengths (see include/rtp.h): step_lens,
+    int32 [B], 0 for the sequences that did not grow."""
+    return _check("rtp_paged_reserve_step", (_lib._native or _lib.native()).reserve(
+        pool.addr, pool.B, pool.device_index, lens, new_lens, counters, lens_out, counters_out,
+        slot_map, n_new, step_lens, ws, _stream_arg(stream)))
 
 
 def _paged_fits(desc: LayerDesc, cache: PagedCache):

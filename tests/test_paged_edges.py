@@ -1,0 +1,39 @@
+"""Refusals and host-side rules of the paged calls at their edges (CPU)."""
+import ctypes
+
+import pytest
+import torch
+
+from long_context_sparse_rtpurbo_b200 import _lib, rtp
+from test_paged_host import X, _pool
+
+
+def test_reserve_step_refusals():
+    """Those of rtp_paged_reserve; step_lens itself may be null."""
+    lib = _lib.load()
+    names = ("lens", "new", "ctr", "lens_out", "ctr_out")
+
+    def call(pool=None, n_new=1, slots=X, step=X, ws=X, wsb=4096, **kw):
+        p = _pool(**(pool or {}))
+        return lib.rtp_paged_reserve_step(ctypes.byref(p), *(kw.get(n, X) for n in names), slots, n_new,
+                                          step, ws, wsb, None)
+
+    for step in (None, X):
+        for n in names:
+            assert call(step=step, **{n: None}) == _lib.RTP_EINVAL, n
+        assert call(step=step, slots=None) == _lib.RTP_EINVAL
+        assert call(dict(B=4097), step=step) == _lib.RTP_ESHAPE
+        assert call(step=step, wsb=4095) == _lib.RTP_EWORKSPACE
+    rtp.rtp_debug_fail_next_call(_lib.RTP_ECUDA)
+    assert call(lens=None) == _lib.RTP_ECUDA
+    assert call(lens=None) == _lib.RTP_EINVAL
+
+
+def test_reserve_step_checks_its_tensor():
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)
+    pool = rtp.make_page_pool(i32(3), i32(2, 4), 16)
+    ctr = torch.zeros(2, dtype=torch.int64)
+    for bad in (i32(3), torch.zeros(2), torch.zeros(2, dtype=torch.int64), i32(4)[::2], 5):
+        with pytest.raises(ValueError, match="step_lens"):
+            rtp.rtp_paged_reserve_step(pool, i32(2), i32(2), ctr, i32(2), ctr, i32(2, 1), 1, bad,
+                                       torch.zeros(4096, dtype=torch.uint8))
