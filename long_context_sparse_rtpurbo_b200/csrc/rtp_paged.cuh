@@ -65,11 +65,17 @@ template <int KV> struct PagedCfg;
 template <> struct PagedCfg<kKvBf16> {
   static constexpr int kWarps = 8, kStages = 3, kRowB = 256, kTerms = 3;
   static constexpr int kStageB = 16 * 512;
+  static constexpr int kLift = 0;
   static constexpr bool kLater = true;         // ranges for the CTAs done first
 };
 template <> struct PagedCfg<kKvE4m3> {
   static constexpr int kWarps = 12, kStages = 4, kRowB = 128, kTerms = 2;
   static constexpr int kStageB = 16 * 256 + 128;
+  // The accumulators' weights are lifted by 2^6: fp16 terms end at 2^-24, so that a row below 2^-25
+  // of the reference would not count in the output (128K such rows under one that weighs 2^26 as
+  // much: 2 % of the output). Lifted, a weight is off by 2^-31 of the reference at most; their
+  // bound of 2^9 becomes 2^15, within fp16.
+  static constexpr int kLift = 6;
   static constexpr bool kLater = false;
 };
 
@@ -455,7 +461,8 @@ __device__ __forceinline__ void tile_issue(const PagedDecodeParams& P, const Til
 
 // Softmax state of a group's heads 2t and 2t + 1 (t = lane % 4) and the O^T accumulators. The
 // weights of the sum l are 2^(z - m). Those of the accumulators are 2^(z + log2(v scale) - mo),
-// with mo = m in a bf16 cache: the references are separate because rows carry their own scale.
+// with mo = m in a bf16 cache: the references are separate because rows carry their own scale, and
+// mo is kLift below the maximum that it stands for.
 template <int KV>
 struct PagedAttn {
   float acc[8][4];
@@ -571,16 +578,18 @@ __device__ __forceinline__ void query_terms(PagedAttn<KV>& A, const QueryRaw& R,
 
 // Moves a reference: x holds this lane's logits of the two heads (rows g, g + 8). It only moves
 // when a logit is more than 2^8 above it (the weights then stay below 2^8), so most tiles cost
-// one vote instead of the maximum over the rows.
+// one vote instead of the maximum over the rows. LIFT: how far the reference lies below the maximum.
+template <int LIFT>
 __device__ __forceinline__ bool move_ref(const float (&x)[4], float (&m)[2], float (&al)[2]) {
-  const bool up = x[0] > m[0] + 8.f || x[2] > m[0] + 8.f || x[1] > m[1] + 8.f || x[3] > m[1] + 8.f;
+  const float t0 = m[0] + (8.f + LIFT), t1 = m[1] + (8.f + LIFT);
+  const bool up = x[0] > t0 || x[2] > t0 || x[1] > t1 || x[3] > t1;
   if (!__any_sync(0xffffffffu, up)) return false;
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     float mx = fmaxf(x[e], x[2 + e]);
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    const float mn = fmaxf(m[e], mx);
+    const float mn = fmaxf(m[e], mx - LIFT);
     al[e] = mn == -INFINITY ? 1.f : ex2(m[e] - mn);
     m[e] = mn;
   }
@@ -651,7 +660,7 @@ __device__ __forceinline__ void paged_tile(PagedAttn<KV>& A, uint32_t stage, uin
     if (!((mask >> (g + 8)) & 1u)) { x[2] = x[3] = -INFINITY; vs[1] = 0.f; }
   }
   float al[2] = {1.f, 1.f};
-  const bool moved = move_ref(x, A.m, al);
+  const bool moved = move_ref<0>(x, A.m, al);
   float p[4];
   {
     const float m0 = A.m[0] == -INFINITY ? 0.f : A.m[0], m1 = A.m[1] == -INFINITY ? 0.f : A.m[1];
@@ -664,18 +673,19 @@ __device__ __forceinline__ void paged_tile(PagedAttn<KV>& A, uint32_t stage, uin
   bool moved_o = moved;
   if (KV == kKvE4m3) {
     // The rows' weights with their scales, against their own reference: 2^(x + log2(vs) - mo) =
-    // p vs 2^(m - mo). A weight above 2^9 moves the reference; so does a factor above 2^64, whose
-    // p could have been too small a number.
+    // p vs 2^(m - mo). A weight above 2^(9 + kLift) moves the reference; so does a factor above 2^64,
+    // whose p could have been too small a number.
     if (moved) { A.cf[0] = ex2(A.m[0] - A.mo[0]); A.cf[1] = ex2(A.m[1] - A.mo[1]); }
     const float f0 = vs[0] * A.cf[0], f1 = vs[0] * A.cf[1], f2 = vs[1] * A.cf[0], f3 = vs[1] * A.cf[1];
     const float w0 = p[0] * f0, w1 = p[1] * f1, w2 = p[2] * f2, w3 = p[3] * f3;
-    const bool far = !((f0 + f1) + (f2 + f3) <= 1.8446744e19f) || !((w0 + w1) + (w2 + w3) <= 512.f);
+    const bool far = !((f0 + f1) + (f2 + f3) <= 1.8446744e19f) ||
+                     !((w0 + w1) + (w2 + w3) <= (float)(512 << Cfg::kLift));
     moved_o = __any_sync(0xffffffffu, far);
     if (moved_o) {
       const float lv0 = lg2(vs[0]), lv1 = lg2(vs[1]);  // -inf for rows that are left out
       const float y[4] = {x[0] + lv0, x[1] + lv0, x[2] + lv1, x[3] + lv1};
       al[0] = al[1] = 1.f;
-      move_ref(y, A.mo, al);
+      move_ref<Cfg::kLift>(y, A.mo, al);
 #pragma unroll
       for (int e = 0; e < 4; ++e) p[e] = ex2_from(y[e], A.mo[e & 1]);
       A.cf[0] = ex2(A.m[0] - A.mo[0]);
@@ -741,6 +751,14 @@ __device__ __forceinline__ int acc_channel(int i, int e) {
   return KV == kKvBf16 ? 16 * i + g + 8 * (e >> 1) : 16 * i + 2 * g + (e >> 1);
 }
 
+// What turns a sum of accumulators into the output: 2^(mo - m) / l, 0 where no row was attended. (The
+// lift is taken out by itself: 2^(mo - m) is flushed to 0 below 2^-126.)
+template <int KV>
+__device__ __forceinline__ float out_factor(float m, float mo, float l) {
+  constexpr int kLift = PagedCfg<KV>::kLift;
+  return l > 0.f || l != l ? ex2_from(mo + kLift, m) / l * (1.f / (1 << kLift)) : 0.f;
+}
+
 // The sum over the rows of each head (a lane has those of rows g and g + 8 of every tile)
 template <int KV>
 __device__ __forceinline__ void attn_sum(PagedAttn<KV>& A) {
@@ -758,8 +776,7 @@ __device__ __forceinline__ void attn_write(const PagedDecodeParams& P, const Pag
   const int64_t head0 = (int64_t)b * P.L.Hq + (int64_t)g * G;
   float f[2];
 #pragma unroll
-  for (int e = 0; e < 2; ++e)
-    f[e] = A.l[e] > 0.f || A.l[e] != A.l[e] ? ex2_from(A.mo[e], A.m[e]) / A.l[e] : 0.f;
+  for (int e = 0; e < 2; ++e) f[e] = out_factor<KV>(A.m[e], A.mo[e], A.l[e]);
   if (P.lse && gr == 0) {
 #pragma unroll
     for (int e = 0; e < 2; ++e)
@@ -1196,7 +1213,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams P) {
           if (first != open_run[0] && first != open_run[1]) {
             const int gd = ent[first].gid, b = small_div(gd, L.Hkv);
             const int64_t head = (int64_t)b * L.Hq + (int64_t)kv_head(L, gd - b * L.Hkv) * G + h;
-            const float f = Ls > 0.f || Ls != Ls ? ex2_from(MO, M) / Ls : 0.f;
+            const float f = out_factor<KV>(M, MO, Ls);
             uint2 w;
             w.x = pack_bf2(s.x * f, s.y * f);
             w.y = pack_bf2(s.z * f, s.w * f);
@@ -1299,7 +1316,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeParams P) {
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) Ls += __shfl_xor_sync(0xffffffffu, Ls, o);
           if (lane == 0) {
-            fac[warp] = Ls > 0.f || Ls != Ls ? ex2_from(MO, M) / Ls : 0.f;
+            fac[warp] = out_factor<KV>(M, MO, Ls);
             if (P.lse) P.lse[head0 + warp] = (M + log2f(Ls)) * 0.6931471805599453f;
           }
         }

@@ -1,4 +1,5 @@
-"""The paged caches where a serving program meets their edges: pools that run out. The models and the
+"""The paged caches where a serving program meets their edges: pools that run out, rows of very
+unequal weight over long lines. Where nothing else is said the models and the
 tolerances of a decode step are those of test_gpu_paged.py."""
 import numpy as np
 import pytest
@@ -123,3 +124,73 @@ def test_a_sequence_that_gets_no_page_is_idle(kv, how):
                 else:
                     assert not out[b, h].any() and float(lse[b, h]) == -np.inf
     assert t.status() == 0 and pl.status() == 0
+
+
+# ------------------------------------------------------------------ one row above a long line
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [4096, 131072])
+def test_decode_dominating_row_over_a_long_line(n, kv):
+    """A first row whose logit is 18 above the others', in groups that lie in a warp or two each: the
+    others weigh 2^-26 of it one by one, and several per cent of the output together. (Every page but
+    the first is the same one.)
+
+    The tolerance. As in test_gpu_paged.py a logit is off by e = 136 * 2^-23 * max S at most, and a
+    weight relatively by d = 2 e + 2^-15 (16-bit terms): that moves the output by d sum_n p_n |v_n - o|.
+    The e4m3 step's weights are two fp16 terms of 2^6 times the weight against a reference that some
+    row has reached: below fp16's normal numbers the second term is off by 2^-25, so each row adds
+    2^-31 max|v|. Sums: two products a tile that may cut, N / 16 * 2^-22 of sum_n p_n |v_n|."""
+    _, _, rtp = _mods()
+    rng = np.random.default_rng(n)
+    page, Hkv, big = 256, 8, 18.0
+    warps = torch.cuda.get_device_properties(0).multi_processor_count * (8 if kv == "bf16" else 12)
+    B = -(-warps // Hkv)
+    q64 = _f64(_bf(rng.normal(size=(Hkv, 128))))
+    z = rng.normal(size=(Hkv, 2 * page))
+    z[:, 0] = big
+    K = np.empty((Hkv, 2 * page, 128))
+    V = 1 + 0.1 * rng.normal(size=(Hkv, 2 * page, 128))
+    V[:, 0] *= 0.05                                       # a sink: small values, but for one channel,
+    V[:, 0, 0] = 1.25                                     # so that its e4m3 scale is the others'
+    k, v = (torch.empty((2, Hkv, page, 128), dtype=torch.bfloat16 if kv == "bf16" else torch.uint8, device=DEV)
+            for _ in range(2))
+    scales = [None, None] if kv == "bf16" else [torch.empty((2, Hkv, page), device=DEV) for _ in range(2)]
+    for g in range(Hkv):
+        qr = rope_rotate(q64[g], n - 1, BASE)
+        K[g] = z[g, :, None] * 128 ** 0.5 * qr / (qr @ qr)
+        for x, dst, sc in ((K, k, scales[0]), (V, v, scales[1])):
+            if kv == "bf16":
+                dst[:, g] = _bf(PO.stored_rows(x[g], kv)).view(2, page, 128)
+            else:
+                r, s = PO.e4m3_rows(x[g])
+                r8 = torch.from_numpy(r.astype(np.float32)).to(DEV).to(torch.float8_e4m3fn)
+                dst[:, g] = r8.view(torch.uint8).view(2, page, 128)
+                sc[:, g] = torch.from_numpy(s.reshape(2, page)).to(DEV)
+            x[g] = PO.stored_rows(x[g], kv)
+    table = np.ones((B, n // page))
+    table[:, 0] = 0
+    desc = rtp.LayerDesc(B, Hkv, Hkv, 0, 1, n, rtp.rtp_build_slot_map([1] * Hkv)[0], BASE)
+    cache = rtp.make_paged_cache(k, v, _i32(table), *scales)
+    ws = torch.empty(rtp.rtp_paged_workspace_bytes(desc), dtype=torch.uint8, device=DEV)
+    rtp.rtp_paged_workspace_init(ws)
+    q = _bf(q64)[None].repeat(B, 1, 1)
+    out, lse = torch.zeros_like(q), torch.zeros((B, Hkv), device=DEV)
+    rtp.rtp_paged_decode_step(desc, cache, q, _i32(np.full(B, n)), out, lse, ws)
+    assert rtp.rtp_read_device_status(ws) == 0
+    times = np.r_[np.ones(page), np.full(page, n // page - 1)]
+    for g in range(Hkv):
+        qr = rope_rotate(q64[g], n - 1, BASE)
+        x = K[g] @ qr / 128 ** 0.5
+        w = times * np.exp(x - x.max())
+        L = w.sum()
+        p = w / L
+        o, e = p @ V[g], x.max() + np.log(L)
+        assert 1 - p[0] > n * 2.0 ** -26                  # the others' share is there to be lost
+        err = 136 * 2.0 ** -23 * (np.abs(K[g]) @ np.abs(qr)).max() / 128 ** 0.5
+        floor = n * 2.0 ** -31 * np.abs(V[g]).max() if kv == "e4m3" else 0.0
+        tol = (2.0 ** -8 * np.abs(o) + (2 * err + 2.0 ** -15) * (p @ np.abs(V[g] - o)) + floor
+               + n / 16 * 2.0 ** -22 * (p @ np.abs(V[g])))
+        d = np.abs(_f64(out)[:, g] - o)
+        assert (d <= tol).all(), (g, (d / np.abs(o)).max(), (d / tol).max())
+        t = err + n / 16 * 2.0 ** -23 + 2.0 ** -21 + 2.0 ** -22 * abs(e)
+        assert np.abs(lse[:, g].double().cpu().numpy() - e).max() <= t
