@@ -40,6 +40,7 @@ class DecodeLayer:
         off = (-self.ws.data_ptr()) % 256
         self.ws = self.ws[off:off + self.ws_bytes]
         rtp.rtp_workspace_init(self.ws)
+        self.zeros = torch.zeros(B, dtype=torch.int32, device=device)   # start of a prompt
 
     def append(self, k_pre, v, w_kidx, start_pos, n_new_b=None, stream=None):
         """k_pre, v: bf16 [B][n_new][Hkv][128]."""
@@ -74,8 +75,7 @@ class DecodeLayer:
         ([B][n_max][Hq][128]). The prefill scratch is allocated on first use and grown with
         the prompt."""
         n_max = q_pre.shape[1]
-        start = torch.zeros(self.B, dtype=torch.int32, device=n_b.device)
-        rtp.rtp_append_kv(self.desc, self.cache, k_pre, v, w_kidx, start, n_b, n_max, self.ws,
+        rtp.rtp_append_kv(self.desc, self.cache, k_pre, v, w_kidx, self.zeros, n_b, n_max, self.ws,
                           stream)
         need = rtp.rtp_prefill_workspace_bytes(self.desc, n_max)
         if need == 0:

@@ -1,0 +1,80 @@
+"""DecodeLayer.prefill and PagedLayer.prefill as a serving program calls them: on other streams."""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+HQ, HKV, CAP = 4, 2, 4096
+
+
+class Prefill:
+    """A layer (two sequences, one retrieval and one local KV head) and prompts of n tokens."""
+
+    def __init__(self, kind, n):
+        from long_context_sparse_rtpurbo_b200 import layer, rtp
+        self.rtp, self.kind, self.n = rtp, kind, n
+        if kind == "paged":
+            self.t = layer.PageTable(2, 2 * CAP // 64, 64, CAP)
+            self.layer = layer.PagedLayer(self.t, HQ, HKV, 4, 128, CAP, [1, 0])
+        else:
+            self.layer = layer.DecodeLayer(2, HQ, HKV, 4, 128, CAP, [1, 0], [CAP, CAP], DEV)
+            self.wk = torch.zeros((HKV, 128, 16), device=DEV)
+        self.inputs(n)
+
+    def inputs(self, n):
+        gen = torch.Generator(device=DEV).manual_seed(n)
+        self.q, self.k, self.v = (torch.randn((2, n, h, 128), dtype=torch.bfloat16, device=DEV, generator=gen)
+                                  for h in (HQ, HKV, HKV))
+        self.n_b = torch.tensor([n, n // 2 + 1], dtype=torch.int32, device=DEV)
+        self.out = torch.zeros_like(self.q)
+        if self.kind == "paged":
+            self.slots = torch.empty((2, n), dtype=torch.int32, device=DEV)
+            self.t.reserve(torch.zeros_like(self.n_b))
+            self.t.reserve(self.n_b, self.slots)
+
+    def run(self, stream=None):
+        if self.kind == "paged":
+            self.layer.prefill(self.q, self.k, self.v, self.n_b, self.slots, self.out, stream)
+        else:
+            self.layer.prefill(self.q, self.k, self.v, self.wk, self.n_b, self.out, stream)
+
+    def cache(self):
+        names = ("k", "v") if self.kind == "paged" else ("k_ret", "v_ret", "k_loc", "v_loc")
+        return [getattr(self.layer, x) for x in names]
+
+    def clear(self):
+        for x in (self.out, *self.cache()):
+            x.zero_()
+
+    def results(self):
+        torch.cuda.synchronize()
+        return [x.clone() for x in (self.out, *self.cache())]
+
+    def ok(self):
+        assert self.layer.status() == 0 and self.rtp.rtp_read_device_status(self.layer.pf_ws) == 0
+
+
+def _same(a, b):
+    return all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("kind", ["contiguous", "paged"])
+def test_prefill_needs_nothing_of_the_current_stream(kind):
+    """A prompt on another stream while the current one is busy for milliseconds: all that the call reads
+    was there before."""
+    n = 700
+    ref = Prefill(kind, n)
+    ref.clear()
+    ref.run()
+    want = ref.results()
+    p = Prefill(kind, n)
+    p.clear()
+    s = torch.cuda.Stream()
+    busy = torch.zeros((8192, 8192), dtype=torch.bfloat16, device=DEV)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        busy = busy @ busy
+    p.run(s)
+    assert _same(p.results(), want)
+    p.ok()
