@@ -9,6 +9,31 @@ import torch
 from . import rtp
 
 
+def _workspace(n, device):
+    """n bytes at a 256-byte boundary."""
+    buf = torch.empty(n + 256, dtype=torch.uint8, device=device)
+    off = (-buf.data_ptr()) % 256
+    return buf[off:off + n]
+
+
+def _prefill_scratch(layer, n_max, device, stream):
+    """layer.pf_ws, large enough for prompts of n_max tokens: allocated on first use, grown with the
+    prompt, always for the stream that the call runs on (a block of another stream's may still be
+    written by what that stream has queued)."""
+    need = rtp.rtp_prefill_workspace_bytes(layer.desc, n_max)
+    if need == 0:
+        raise ValueError("librtp rejected the prompt length")
+    used = torch.cuda.current_stream(device) if stream is None else stream
+    if not hasattr(used, "cuda_stream"):
+        used = torch.cuda.ExternalStream(int(used), device=device)
+    if layer.pf_ws is None or layer.pf_ws.numel() < need:
+        with torch.cuda.stream(used):
+            layer.pf_ws = _workspace(need, device)
+    # a later, longer prompt lets go of this buffer: not before this call's stream is done
+    layer.pf_ws.record_stream(used)
+    return layer.pf_ws
+
+
 class DecodeLayer:
     def __init__(self, B, Hq, Hkv, sinks, window, max_seq_len, ret_mask, seq_caps,
                  device="cuda", rope_base=1e6):
@@ -41,6 +66,7 @@ class DecodeLayer:
         self.ws = self.ws[off:off + self.ws_bytes]
         rtp.rtp_workspace_init(self.ws)
         self.zeros = torch.zeros(B, dtype=torch.int32, device=device)   # start of a prompt
+        self.pf_ws = None
 
     def append(self, k_pre, v, w_kidx, start_pos, n_new_b=None, stream=None):
         """k_pre, v: bf16 [B][n_new][Hkv][128]."""
@@ -77,25 +103,11 @@ class DecodeLayer:
         n_max = q_pre.shape[1]
         rtp.rtp_append_kv(self.desc, self.cache, k_pre, v, w_kidx, self.zeros, n_b, n_max, self.ws,
                           stream)
-        need = rtp.rtp_prefill_workspace_bytes(self.desc, n_max)
-        if need == 0:
-            raise ValueError("librtp rejected the prompt length")
-        if getattr(self, "pf_ws", None) is None or self.pf_ws.numel() < need:
-            buf = torch.empty(need + 256, dtype=torch.uint8, device=q_pre.device)
-            off = (-buf.data_ptr()) % 256
-            self.pf_ws = buf[off:off + need]
-        return rtp.rtp_prefill(self.desc, q_pre, k_pre, v, n_b, n_max, out, self.pf_ws,
-                               self.pf_ws.numel(), stream)
+        ws = _prefill_scratch(self, n_max, q_pre.device, stream)
+        return rtp.rtp_prefill(self.desc, q_pre, k_pre, v, n_b, n_max, out, ws, ws.numel(), stream)
 
     def status(self, stream=None) -> int:
         return rtp.rtp_read_device_status(self.ws, stream)
-
-
-def _workspace(n, device):
-    """n bytes at a 256-byte boundary."""
-    buf = torch.empty(n + 256, dtype=torch.uint8, device=device)
-    off = (-buf.data_ptr()) % 256
-    return buf[off:off + n]
 
 
 class PageTable:
@@ -183,18 +195,8 @@ class PagedLayer:
         n_max = q_pre.shape[1]
         rtp.rtp_paged_append_kv(self.desc, self.cache, k_pre, v, self.zeros, slot_map, n_max,
                                 self.ws, stream)
-        need = rtp.rtp_prefill_workspace_bytes(self.desc, n_max)
-        if need == 0:
-            raise ValueError("librtp rejected the prompt length")
-        if self.pf_ws is None or self.pf_ws.numel() < need:
-            self.pf_ws = _workspace(need, q_pre.device)
-        # a later, longer prompt lets go of this buffer: not before this call's stream is done
-        used = torch.cuda.current_stream() if stream is None else stream
-        if not hasattr(used, "cuda_stream"):
-            used = torch.cuda.ExternalStream(int(used))
-        self.pf_ws.record_stream(used)
-        return rtp.rtp_prefill(self.desc, q_pre, k_pre, v, n_b, n_max, out, self.pf_ws,
-                               self.pf_ws.numel(), stream)
+        ws = _prefill_scratch(self, n_max, q_pre.device, stream)
+        return rtp.rtp_prefill(self.desc, q_pre, k_pre, v, n_b, n_max, out, ws, ws.numel(), stream)
 
     def status(self, stream=None) -> int:
         return rtp.rtp_read_device_status(self.ws, stream)

@@ -78,3 +78,31 @@ def test_prefill_needs_nothing_of_the_current_stream(kind):
     p.run(s)
     assert _same(p.results(), want)
     p.ok()
+
+
+@pytest.mark.parametrize("kind", ["contiguous", "paged"])
+@pytest.mark.parametrize("how", ["stream", "address", "current"])
+def test_scratch_comes_from_the_calls_stream(kind, how):
+    """A block of the scratch's very size that the current stream has let go of, with work on it maybe
+    still queued there, is not the one that a call on another stream gets."""
+    n = 3000
+    ref = Prefill(kind, n)
+    ref.clear()
+    ref.run()
+    want = ref.results()
+    p = Prefill(kind, n)
+    p.clear()
+    size = p.rtp.rtp_prefill_workspace_bytes(p.layer.desc, n) + 256
+    block = torch.zeros(size, dtype=torch.uint8, device=DEV)
+    torch.cuda.synchronize()
+    lo = block.data_ptr()
+    del block
+    s = torch.cuda.Stream()
+    if how == "current":
+        with torch.cuda.stream(s):
+            p.run()
+    else:
+        p.run(s if how == "stream" else s.cuda_stream)
+    assert not lo <= p.layer.pf_ws.data_ptr() < lo + size
+    assert _same(p.results(), want)
+    p.ok()
