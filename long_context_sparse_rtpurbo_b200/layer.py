@@ -19,16 +19,19 @@ def _workspace(n, device):
 def _prefill_scratch(layer, n_max, device, stream):
     """layer.pf_ws, large enough for prompts of n_max tokens: allocated on first use, grown with the
     prompt, always for the stream that the call runs on (a block of another stream's may still be
-    written by what that stream has queued)."""
+    written by what that stream has queued). A captured graph holds the address of its scratch, so
+    that one stays allocated with the layer (pf_held) when a longer prompt gets another."""
     need = rtp.rtp_prefill_workspace_bytes(layer.desc, n_max)
     if need == 0:
         raise ValueError("librtp rejected the prompt length")
     used = torch.cuda.current_stream(device) if stream is None else stream
     if not hasattr(used, "cuda_stream"):
         used = torch.cuda.ExternalStream(int(used), device=device)
-    if layer.pf_ws is None or layer.pf_ws.numel() < need:
-        with torch.cuda.stream(used):
+    with torch.cuda.stream(used):
+        if layer.pf_ws is None or layer.pf_ws.numel() < need:
             layer.pf_ws = _workspace(need, device)
+        if torch.cuda.is_current_stream_capturing() and not any(x is layer.pf_ws for x in layer.pf_held):
+            layer.pf_held.append(layer.pf_ws)
     # a later, longer prompt lets go of this buffer: not before this call's stream is done
     layer.pf_ws.record_stream(used)
     return layer.pf_ws
@@ -66,7 +69,7 @@ class DecodeLayer:
         self.ws = self.ws[off:off + self.ws_bytes]
         rtp.rtp_workspace_init(self.ws)
         self.zeros = torch.zeros(B, dtype=torch.int32, device=device)   # start of a prompt
-        self.pf_ws = None
+        self.pf_ws, self.pf_held = None, []
 
     def append(self, k_pre, v, w_kidx, start_pos, n_new_b=None, stream=None):
         """k_pre, v: bf16 [B][n_new][Hkv][128]."""
@@ -166,7 +169,7 @@ class PagedLayer:
         self.ws = _workspace(n, device)
         rtp.rtp_paged_workspace_init(self.ws)
         self.zeros = torch.zeros(table.B, dtype=torch.int32, device=device)
-        self.pf_ws = None
+        self.pf_ws, self.pf_held = None, []
 
     def append(self, k_pre, v, start_pos, slot_map, stream=None):
         """k_pre, v: bf16 [B][n_new][Hkv][128]; start_pos: int32 [B], the lengths before the

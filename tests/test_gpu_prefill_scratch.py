@@ -1,4 +1,5 @@
-"""DecodeLayer.prefill and PagedLayer.prefill as a serving program calls them: on other streams."""
+"""DecodeLayer.prefill and PagedLayer.prefill as a serving program calls them: on other streams, in
+captured graphs."""
 import numpy as np
 import pytest
 import torch
@@ -105,4 +106,46 @@ def test_scratch_comes_from_the_calls_stream(kind, how):
         p.run(s if how == "stream" else s.cuda_stream)
     assert not lo <= p.layer.pf_ws.data_ptr() < lo + size
     assert _same(p.results(), want)
+    p.ok()
+
+
+@pytest.mark.parametrize("kind", ["contiguous", "paged"])
+@pytest.mark.parametrize("warm", [True, False])
+def test_a_graphs_scratch_outlives_a_longer_prompt(kind, warm):
+    """A captured prompt, then a longer one that needs more scratch, then tensors of the size of the
+    first scratch: a replay gives the results again and writes to none of them. The scratch is made
+    before the capture or in it."""
+    Prefill(kind, 500).run()                              # (loads every kernel)
+    p, ref = Prefill(kind, 500), Prefill(kind, 500)
+    ref.clear()
+    ref.run()
+    want = ref.results()
+    if warm:
+        p.run()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        p.run()
+    first = p.layer.pf_ws
+    lo, size = first.data_ptr(), first.numel()
+    del first
+    kept = {x: getattr(p, x) for x in ("q", "k", "v", "n_b", "out") + (("slots",) if kind == "paged" else ())}
+    p.inputs(1500)
+    p.run()
+    assert p.layer.pf_ws.numel() > size
+    others = [torch.full((size + 256 * i,), 0xA5, dtype=torch.uint8, device=DEV) for i in (0, 1, 1, 1)]
+    assert not any(x.data_ptr() < lo + size and lo < x.data_ptr() + x.numel() for x in others)
+    torch.cuda.synchronize()
+    for x, t in kept.items():
+        setattr(p, x, t)
+    if kind == "paged":                                   # the prompt's own pages again
+        p.t.reserve(torch.zeros_like(p.n_b))
+        p.t.reserve(p.n_b, p.slots)
+    p.clear()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(p.out, want[0])
+    if kind == "contiguous":                              # (pages are other ones by now)
+        assert _same(p.cache(), want[1:])
+    assert all((x == 0xA5).all() for x in others)
     p.ok()
