@@ -45,21 +45,32 @@ struct Plan {
       off_trace, total;
 };
 
-// theta_i = base^(-2i/d), and (cos, sin) of 1, 2 and 4 theta_i: library calls, so the last
-// base's are kept per thread
-struct RopeTables { double base = 0.0, theta[kD / 2]; double2 turn[3][kD / 2]; };
-const RopeTables& rope_tables(double base) {
-  static thread_local RopeTables t;
-  if (t.base != base) {
-    for (int i = 0; i < kD / 2; ++i) {
-      t.theta[i] = std::pow(base, -2.0 * i / (double)kD);
-      for (int k = 0; k < 3; ++k) {
-        const double x = t.theta[i] * (1 << k);
-        t.turn[k][i] = make_double2(std::cos(x), std::sin(x));
-      }
+// theta_i = base^(-2i/d), and for the paged append (cos, sin) of 1, 2 and 4 theta_i: library calls
+// (1.1 and 2.4 us a set), so the last bases' are kept per thread, for models whose layers have two
+// or more
+struct RopeTables { double base = 0.0, theta[kD / 2]; bool turned = false; double2 turn[3][kD / 2]; };
+RopeTables& rope_tables(double base) {
+  constexpr int kKept = 4;
+  static thread_local RopeTables kept[kKept];
+  static thread_local int next = 0;
+  for (RopeTables& t : kept)
+    if (t.base == base) return t;
+  RopeTables& t = kept[next];
+  next = (next + 1) % kKept;
+  for (int i = 0; i < kD / 2; ++i) t.theta[i] = std::pow(base, -2.0 * i / (double)kD);
+  t.turned = false;
+  t.base = base;
+  return t;
+}
+const RopeTables& rope_turns(double base) {
+  RopeTables& t = rope_tables(base);
+  if (t.turned) return t;
+  for (int i = 0; i < kD / 2; ++i)
+    for (int k = 0; k < 3; ++k) {
+      const double x = t.theta[i] * (1 << k);
+      t.turn[k][i] = make_double2(std::cos(x), std::sin(x));
     }
-    t.base = base;
-  }
+  t.turned = true;
   return t;
 }
 
@@ -755,7 +766,7 @@ int rtp_paged_append_kv(const rtp_layer_desc* desc, const rtp_paged_cache* cache
   P.inv_last = (65536u + last - 1) / last;
   P.step_last = 8 / last;
   P.status = static_cast<int*>(ws);
-  const RopeTables& rt = rope_tables(desc->rope_base);
+  const RopeTables& rt = rope_turns(desc->rope_base);
   memcpy(P.theta, rt.theta, sizeof(P.theta));
   // R = 2 or 4 (for few rows a token) shares a sine among neighbouring tokens: 32K tokens of 8 KV
   // heads take 50, 43 and 46 us with R = 1, 2 and 4, of 4 heads 37, 27 and 24. Calls of fewer than

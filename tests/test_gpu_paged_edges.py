@@ -194,3 +194,27 @@ def test_decode_dominating_row_over_a_long_line(n, kv):
         assert (d <= tol).all(), (g, (d / np.abs(o)).max(), (d / tol).max())
         t = err + n / 16 * 2.0 ** -23 + 2.0 ** -21 + 2.0 ** -22 * abs(e)
         assert np.abs(lse[:, g].double().cpu().numpy() - e).max() <= t
+
+
+# ------------------------------------------------------------------ layers of several RoPE bases
+
+def test_append_with_many_rope_bases():
+    """Appends of layers that take turns with six RoPE bases, more than are kept: rows against the
+    formula in 64 bits, half a bf16 step and 2^-40 for the angles."""
+    _, _, rtp = _mods()
+    rng = np.random.default_rng(71)
+    B, n, Hkv, page, start = 1, 900, 4, 64, 5000
+    slots = _i32(np.arange(n)[None])
+    for i in range(12):
+        base = [1e4, 1e6, 5e5, 1e7, 2.0, 1e5][i % 6]
+        kp, vp = (_bf(rng.normal(size=(B, n, Hkv, 128))) for _ in range(2))
+        k, v = (torch.zeros((-(-n // page), Hkv, page, 128), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+        desc = rtp.LayerDesc(B, Hkv, Hkv, 0, 1, 1 << 20, rtp.rtp_build_slot_map([1] * Hkv)[0], base)
+        cache = rtp.make_paged_cache(k, v, torch.zeros((B, 1), dtype=torch.int32, device=DEV))
+        rtp.rtp_paged_append_kv(desc, cache, kp, vp, _i32([start]), slots, n)
+        a = (start + np.arange(n))[:, None, None] * base ** (-np.arange(64) / 64.0)
+        x = _f64(kp)[0]
+        want = np.concatenate([x[..., :64] * np.cos(a) - x[..., 64:] * np.sin(a),
+                               x[..., :64] * np.sin(a) + x[..., 64:] * np.cos(a)], -1)
+        got = _f64(k).swapaxes(1, 2).reshape(-1, Hkv, 128)[:n]
+        assert (np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -40).all(), base

@@ -1,5 +1,6 @@
 """Refusals and host-side rules of the paged calls at their edges (CPU)."""
 import ctypes
+import time
 
 import pytest
 import torch
@@ -37,3 +38,25 @@ def test_reserve_step_checks_its_tensor():
         with pytest.raises(ValueError, match="step_lens"):
             rtp.rtp_paged_reserve_step(pool, i32(2), i32(2), ctr, i32(2), ctr, i32(2, 1), 1, bad,
                                        torch.zeros(4096, dtype=torch.uint8))
+
+
+def test_layers_of_two_rope_bases_cost_no_more():
+    """A description's check costs the same whether the call before had another RoPE base or not (it
+    took 6 times as long while one base's tables were kept). The least of many runs, with a factor of
+    three for noise."""
+    slots = rtp.rtp_build_slot_map([1, 0])[0]
+    a, b = (rtp.LayerDesc(1, 4, 2, 4, 64, 64, slots, base) for base in (1e4, 1e6))
+    check = _lib.load().rtp_paged_workspace_bytes
+
+    def cost(first, second):
+        best = 1e9
+        for _ in range(40):
+            t0 = time.perf_counter()
+            for _ in range(100):
+                check(first.ref)
+                check(second.ref)
+            best = min(best, time.perf_counter() - t0)
+        return best
+
+    assert check(a.ref) == check(b.ref) > 0
+    assert cost(a, b) < 3 * cost(a, a)
