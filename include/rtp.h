@@ -315,6 +315,7 @@ int rtp_paged_reserve_step(const rtp_page_pool* pool, const int32_t* lens, const
  *   start_pos : [B]; token j of sequence b is at position start_pos[b] + j.
  *   slot_map  : [B][n_new] slots, all different; a token with a negative slot is skipped.
  *   ws        : status word (4 bytes; may be NULL).
+ * n_new == 0 does nothing; the arrays may be NULL then.
  * RTP_KV_BF16: the rows that rtp_append_kv writes, bit for bit (R(pos) k_pre evaluated in double
  * precision, rounded once; v). RTP_KV_E4M3: with x the row in single precision (the rotated key
  * rounded once), scale = max(max|x| / 448, 2^-126) and bytes x / scale, to nearest even.

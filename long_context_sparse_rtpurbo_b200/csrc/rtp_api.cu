@@ -753,10 +753,10 @@ int rtp_paged_append_kv(const rtp_layer_desc* desc, const rtp_paged_cache* cache
   PagedAppendParams P;
   rc = check_paged(cache, L.Hkv, P.C);
   if (rc != RTP_OK) return rc;
+  if (n_new == 0) return RTP_OK;                       // (empty arrays have no address)
   if (!k_pre || !v || !start_pos || !slot_map || n_new < 0) return RTP_EINVAL;
   if (!al16(k_pre) || !al16(v)) return RTP_EINVAL;
   if ((reinterpret_cast<uintptr_t>(ws) & 3) != 0) return RTP_EWORKSPACE;
-  if (n_new == 0) return RTP_OK;
   P.k_pre = k_pre; P.v = v; P.start_pos = start_pos; P.slot_map = slot_map;
   P.n_new = n_new; P.n_tok = (int64_t)L.B * n_new;
   P.cap_rows = (int64_t)P.C.n_pages << P.C.lg;

@@ -218,3 +218,19 @@ def test_append_with_many_rope_bases():
                                x[..., :64] * np.sin(a) + x[..., 64:] * np.cos(a)], -1)
         got = _f64(k).swapaxes(1, 2).reshape(-1, Hkv, 128)[:n]
         assert (np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -40).all(), base
+
+
+# ------------------------------------------------------------------ nothing to append
+
+def test_calls_of_no_tokens():
+    """An empty chunk through the layer: an append of [B][0] tokens, a reservation without new tokens."""
+    _, layer, rtp = _mods()
+    t = layer.PageTable(2, 4, 16, 64)
+    pl = layer.PagedLayer(t, 4, 2, 2, 20, 64, [1, 0])
+    pl.k.zero_()
+    t.reserve(_i32([5, 0]), torch.empty((2, 0), dtype=torch.int32, device=DEV))
+    assert t.lens.tolist() == [5, 0] and t.step_lens.tolist() == [5, 0]
+    rows = torch.empty((2, 0, 2, 128), dtype=torch.bfloat16, device=DEV)
+    pl.append(rows, rows, t.lens, torch.empty((2, 0), dtype=torch.int32, device=DEV))
+    assert rtp.rtp_last_launch_count() == 0
+    assert t.status() == 0 and pl.status() == 0 and not pl.k.any()

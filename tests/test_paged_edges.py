@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from long_context_sparse_rtpurbo_b200 import _lib, rtp
-from test_paged_host import X, _pool
+from test_paged_host import X, _cache, _desc, _pool
 
 
 def test_reserve_step_refusals():
@@ -60,3 +60,11 @@ def test_layers_of_two_rope_bases_cost_no_more():
 
     assert check(a.ref) == check(b.ref) > 0
     assert cost(a, b) < 3 * cost(a, a)
+
+
+def test_append_of_no_tokens_does_nothing():
+    """Arrays of no elements have no address. The description and the cache are checked all the same."""
+    lib, d, c = _lib.load(), _desc(), _cache()
+    call = lambda c: lib.rtp_paged_append_kv(d.ref, ctypes.byref(c), None, None, X, None, 0, None, None)
+    assert call(c) == _lib.RTP_OK and rtp.rtp_last_launch_count() == 0
+    assert call(_cache(page_size=8)) == _lib.RTP_ESHAPE
