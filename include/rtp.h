@@ -222,8 +222,12 @@ int rtp_prefill(const rtp_layer_desc* desc, const uint16_t* q_pre, const uint16_
  * g * page_size + n % page_size of that page. All KV heads of a layer, local ones too, keep every
  * position (a local head reads its sinks and window only). A slot is page * page_size + row.
  * Entries of block_table behind a sequence's last page are not read. Several sequences may
- * share pages (a common prefix) as long as no call writes to a shared page. Outputs overlap inputs
- * only where a call says so.
+ * share pages (a common prefix) in the table of a cache, as long as no call writes to a shared
+ * page. In the table of a page pool every page belongs to one sequence: rtp_paged_reserve counts no
+ * references, and a page that two sequences of the pool held would be handed out twice once both
+ * have ended. So a shared prefix (whole pages) is a sequence of the pool by itself, which ends after
+ * the ones that use it; theirs hold the rest, and the caller puts the prefix's pages before them
+ * in the table that the cache is given. Outputs overlap inputs only where a call says so.
  */
 enum {
   RTP_KV_BF16 = 0,      /* rows of 128 bf16 */
@@ -274,6 +278,7 @@ int rtp_paged_workspace_init(void* ws, size_t ws_bytes, rtp_stream_t stream);
  * Block tables and slot maps for new lengths, on the GPU (one launch).
  *   lens, new_lens : [B] tokens that the sequences hold now and shall hold. A sequence holds
  *                    ceil(len / page_size) pages, the first entries of its block-table row.
+ * No page is held twice in pool->block_table (see above).
  *   counters       : [2] {head, tail}: the ring's free pages are free_pages[i % n_pages] for
  *                    head <= i < tail. Both only grow. A new pool: all ids, {0, n_pages}.
  *   lens_out       : [B] lengths after the call: new_lens[b] where the sequence was served,

@@ -115,7 +115,9 @@ class DecodeLayer:
 
 class PageTable:
     """The pages of a batch of B sequences, shared by the layers of a model: lengths, block
-    table and ring of free pages, all on the GPU. A sequence holds at most max_seq_len tokens."""
+    table and ring of free pages, all on the GPU. A sequence holds at most max_seq_len tokens, in pages
+    of its own: references are not counted, so block_table never has a page twice (a shared prefix
+    goes into another table, see include/rtp.h)."""
 
     def __init__(self, B, n_pages, page_size, max_seq_len, device="cuda"):
         i32 = dict(dtype=torch.int32, device=device)

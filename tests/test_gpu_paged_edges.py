@@ -1,5 +1,5 @@
 """The paged caches where a serving program meets their edges: pools that run out, rows of very
-unequal weight over long lines. Where nothing else is said the models and the
+unequal weight over long lines, shared prefixes. Where nothing else is said the models and the
 tolerances of a decode step are those of test_gpu_paged.py."""
 import numpy as np
 import pytest
@@ -234,3 +234,50 @@ def test_calls_of_no_tokens():
     pl.append(rows, rows, t.lens, torch.empty((2, 0), dtype=torch.int32, device=DEV))
     assert rtp.rtp_last_launch_count() == 0
     assert t.status() == 0 and pl.status() == 0 and not pl.k.any()
+
+
+# ------------------------------------------------------------------ a shared prefix
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_shared_prefix_is_a_sequence_of_its_own(kv):
+    """Two sequences behind a common prefix of two pages, as the header has it: the prefix is a third
+    sequence of the pool, and a table of the caller's puts its pages before theirs. Steps over that
+    table against the model; in the end every page is free once."""
+    _, layer, rtp = _mods()
+    rng = np.random.default_rng(72)
+    Hq, Hkv, page, cap, sinks, window, pre = 8, 2, 16, 96, 2, 20, 32
+    dt = torch.bfloat16 if kv == "bf16" else torch.float8_e4m3fn
+    t = layer.PageTable(3, 9, page, cap)                  # sequences 0 and 1, the prefix
+    pl = layer.PagedLayer(t, Hq, Hkv, sinks, window, cap, [1, 0], dt, BASE)
+    kp, vp = (_bf(rng.normal(size=(3, pre, Hkv, 128))) for _ in range(2))
+    slots = torch.empty((3, pre), dtype=torch.int32, device=DEV)
+    t.reserve(_i32([0, 0, pre]), slots)
+    pl.append(kp, vp, pl.zeros, slots)
+    both = torch.full((2, 6), -1, dtype=torch.int32, device=DEV)
+    both[:, :2] = t.block_table[2, :2]
+    cache = rtp.make_paged_cache(pl.k, pl.v, both, pl.k_scale, pl.v_scale)
+    desc = rtp.LayerDesc(2, Hq, Hkv, sinks, window, cap, rtp.rtp_build_slot_map([1, 0])[0], BASE)
+    K = {(b, g): [rope_rotate(_f64(kp)[2, j, g], j, BASE) for j in range(pre)] for b in range(2) for g in range(Hkv)}
+    V = {(b, g): list(_f64(vp)[2, :, g]) for b in range(2) for g in range(Hkv)}
+    c = Case.__new__(Case)
+    c.G, c.ret, c.sinks, c.window = Hq // Hkv, [True, False], sinks, window
+    for i in range(20):
+        n = i + 1
+        t.reserve(_i32([n, max(0, n - 3), pre]))          # sequence 1 starts three steps later
+        both[:, 2:5] = t.block_table[:2, :3]
+        lens = torch.where(t.step_lens[:2] > 0, t.step_lens[:2] + pre, 0)
+        q, k, v = (_bf(rng.normal(size=(2, h, 128))) for h in (Hq, Hkv, Hkv))
+        out, lse = torch.zeros_like(q), torch.zeros((2, Hq), device=DEV)
+        rtp.rtp_paged_decode_step_append(desc, cache, k, v, q, lens, out, lse, pl.ws)
+        c.q64 = _f64(q)
+        for b, m in enumerate(lens.tolist()):
+            for g in range(Hkv if m else 0):
+                K[b, g].append(rope_rotate(_f64(k)[b, g], m - 1, BASE))
+                V[b, g].append(_f64(v)[b, g])
+        c.rows = {name: {key: PO.stored_rows(np.array(r), kv) for key, r in rs.items()} for name, rs in (("k", K), ("v", V))}
+        for b, m in enumerate(lens.tolist()):
+            for h in range(Hq if m else 0):
+                c.agree(_f64(out)[b, h], float(lse[b, h]), b, h, m)
+    t.reserve(_i32([0, 0, 0]))
+    free = [int(t.free_pages[i % 9]) for i in range(*t.counters.tolist())]
+    assert sorted(free) == list(range(9)) and t.status() == 0 and pl.status() == 0
