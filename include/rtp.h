@@ -321,9 +321,12 @@ int rtp_paged_reserve_step(const rtp_page_pool* pool, const int32_t* lens, const
  *   slot_map  : [B][n_new] slots, all different; a token with a negative slot is skipped.
  *   ws        : status word (4 bytes; may be NULL).
  * n_new == 0 does nothing; the arrays may be NULL then.
- * RTP_KV_BF16: the rows that rtp_append_kv writes, bit for bit (R(pos) k_pre evaluated in double
- * precision, rounded once; v). RTP_KV_E4M3: with x the row in single precision (the rotated key
- * rounded once), scale = max(max|x| / 448, 2^-126) and bytes x / scale, to nearest even.
+ * RTP_KV_BF16: R(pos) k_pre evaluated in double precision and rounded once, and v. These are the
+ * rows that rtp_append_kv writes, but for keys so near the border of two bf16 values that the last
+ * places of the angle decide: up to eight neighbouring tokens of a sequence share a sine, turned on
+ * by products in double, which moves a key by up to (2^-52 pos + 2^-50) of its pair's length.
+ * RTP_KV_E4M3: with x the row in single precision (the rotated key rounded once), scale =
+ * max(max|x| / 448, 2^-126) and bytes x / scale, to nearest even.
  * A slot outside the pages or a negative position is skipped and sets RTP_EDEVICE.
  */
 int rtp_paged_append_kv(const rtp_layer_desc* desc, const rtp_paged_cache* cache,

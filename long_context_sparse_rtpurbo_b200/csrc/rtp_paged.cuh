@@ -1392,7 +1392,8 @@ struct PagedAppendParams {
 // A CTA of 128 threads takes up to 8 KV heads of 2 R consecutive tokens of the flattened
 // [B][n_new] axis. Their rows, contiguous in the inputs, are copied to shared memory while the
 // angles are made, once for all heads: sin and cos in double of the first token's 64 angles, the
-// other tokens of its sequence by turning on (products of cos and sin of theta). Then half a warp
+// other tokens of its sequence by turning on (products of cos and sin of theta: off by 2^-50, where
+// position * theta itself is rounded by up to 2^-53 of its size). Then half a warp
 // per (token, KV head) row, 4 channel pairs a lane, in double. (Eight CTAs an SM, each at another
 // of these stages; 256 threads and twice the tokens were 2 to 7 % slower.)
 // Bound by HBM: 512 B read, 512 (264) B written per row; bf16 rows run at it (32K tokens of 8 KV

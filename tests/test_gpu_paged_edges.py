@@ -281,3 +281,40 @@ def test_shared_prefix_is_a_sequence_of_its_own(kv):
     t.reserve(_i32([0, 0, 0]))
     free = [int(t.free_pages[i % 9]) for i in range(*t.counters.tolist())]
     assert sorted(free) == list(range(9)) and t.status() == 0 and pl.status() == 0
+
+
+# ------------------------------------------------------------------ paged and contiguous appends
+
+@pytest.mark.parametrize("n", [1, 2, 40, 4099])
+def test_append_rows_next_to_the_contiguous_ones(n):
+    """Rows at far positions against rtp_append_kv's, in calls that share a sine among one, two, four and
+    eight tokens. One token: the same bits. Otherwise a key may differ where it lies next to the middle
+    of two bf16 values: turned-on angles differ by pos 2^-52 + 2^-50 (two roundings of position *
+    theta, and a few of the products), and the value formed here by as much again."""
+    _, layer, rtp = _mods()
+    rng = np.random.default_rng(n)
+    B, Hkv, page, start = 1, 4, 128, 1_000_003
+    end = start + n
+    kp, vp = (_bf(rng.normal(size=(B, n, Hkv, 128))) for _ in range(2))
+    lay = layer.DecodeLayer(B, Hkv, Hkv, 4, 64, end, [1] * Hkv, [end], DEV, BASE)
+    lay.append(kp, vp, torch.zeros((Hkv, 128, 16), device=DEV), _i32([start]))
+    k, v = (torch.zeros((-(-n // page), Hkv, page, 128), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    desc = rtp.LayerDesc(B, Hkv, Hkv, 4, 64, end, rtp.rtp_build_slot_map([1] * Hkv)[0], BASE)
+    cache = rtp.make_paged_cache(k, v, torch.zeros((B, 1), dtype=torch.int32, device=DEV))
+    rtp.rtp_paged_append_kv(desc, cache, kp, vp, _i32([start]), _i32(np.arange(n)[None]), n)
+    flat = lambda x: _f64(x).swapaxes(1, 2).reshape(-1, Hkv, 128)[:n]
+    theirs = lambda x: _f64(x[:, start:end]).swapaxes(0, 1)
+    assert np.array_equal(flat(v), theirs(lay.v_ret)) and lay.status() == 0
+    a, b = flat(k), theirs(lay.k_ret)
+    bad = a != b
+    if n == 1:
+        assert not bad.any()
+    pos = start + np.arange(n)
+    ang = pos[:, None, None] * BASE ** (-np.arange(64) / 64.0)
+    x = _f64(kp)[0]
+    u, w = x[..., :64], x[..., 64:]
+    want = np.concatenate([u * np.cos(ang) - w * np.sin(ang), u * np.sin(ang) + w * np.cos(ang)], -1)
+    length = np.tile(np.hypot(u, w), 2)
+    room = 2 * (2.0 ** -52 * pos[:, None, None] + 2.0 ** -50) * length
+    assert (np.abs(want - (a + b) / 2)[bad] <= room[bad]).all()
+    assert bad.sum() <= 1e-6 * bad.size + 1
