@@ -3,6 +3,7 @@
 from __future__ import annotations
 
 import os
+import shutil
 import subprocess
 import sysconfig
 
@@ -16,6 +17,17 @@ def nvcc() -> str:
         if c and (os.path.sep not in c or os.path.exists(c)):
             return c
     return "nvcc"
+
+
+def cuda_include() -> str:
+    """The headers of the toolkit that nvcc belongs to."""
+    exe = shutil.which(nvcc())
+    home = os.path.dirname(os.path.dirname(os.path.realpath(exe))) if exe else "/usr/local/cuda"
+    for inc in (os.path.join(home, "include"), os.path.join(home, "targets", "x86_64-linux", "include"),
+                "/usr/local/cuda/include"):
+        if os.path.exists(os.path.join(inc, "cuda_runtime_api.h")):
+            return inc
+    raise RuntimeError(f"cuda_runtime_api.h not found beside {exe or 'nvcc'}")
 
 
 def build(verbose: bool = False, extra_flags=(), out_name: str = "librtp.so") -> str:
@@ -43,7 +55,7 @@ def build_binding(verbose: bool = False) -> str:
     import torch
     from torch.utils import cpp_extension as ext
     out = os.path.join(HERE, "_binding.so")
-    inc = [sysconfig.get_paths()["include"], "/usr/local/cuda/include", *ext.include_paths()]
+    inc = [sysconfig.get_paths()["include"], cuda_include(), *ext.include_paths()]
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",

@@ -1,5 +1,6 @@
 """Refusals and host-side rules of the paged calls at their edges (CPU)."""
 import ctypes
+import os
 import time
 
 import pytest
@@ -68,3 +69,28 @@ def test_append_of_no_tokens_does_nothing():
     call = lambda c: lib.rtp_paged_append_kv(d.ref, ctypes.byref(c), None, None, X, None, 0, None, None)
     assert call(c) == _lib.RTP_OK and rtp.rtp_last_launch_count() == 0
     assert call(_cache(page_size=8)) == _lib.RTP_ESHAPE
+
+
+def test_binding_is_built_with_the_toolkit_of_nvcc(tmp_path, monkeypatch):
+    """A toolkit in another place than /usr/local/cuda, named by NVCC or found through the path."""
+    from long_context_sparse_rtpurbo_b200 import build
+    home = tmp_path / "cuda"
+    for d in ("bin", "include"):
+        (home / d).mkdir(parents=True)
+    (home / "bin" / "nvcc").write_text("#!/bin/sh\n")
+    (home / "bin" / "nvcc").chmod(0o755)
+    (home / "include" / "cuda_runtime_api.h").write_text("")
+    ran = []
+    monkeypatch.setattr(build.subprocess, "run", lambda cmd, **kw: ran.append(cmd))
+    monkeypatch.setenv("NVCC", str(home / "bin" / "nvcc"))
+    build.build_binding()
+    assert f"-I{home / 'include'}" in ran[0] and "-I/usr/local/cuda/include" not in ran[0]
+    link = tmp_path / "nvcc"                                 # a link to it somewhere on the path
+    os.symlink(home / "bin" / "nvcc", link)
+    monkeypatch.setenv("NVCC", str(link))
+    assert build.cuda_include() == str(home / "include")
+    (home / "include" / "cuda_runtime_api.h").unlink()
+    inner = home / "targets" / "x86_64-linux" / "include"
+    inner.mkdir(parents=True)
+    (inner / "cuda_runtime_api.h").write_text("")
+    assert build.cuda_include() == str(inner)
