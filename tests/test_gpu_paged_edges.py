@@ -318,3 +318,109 @@ def test_append_rows_next_to_the_contiguous_ones(n):
     room = 2 * (2.0 ** -52 * pos[:, None, None] + 2.0 ** -50) * length
     assert (np.abs(want - (a + b) / 2)[bad] <= room[bad]).all()
     assert bad.sum() <= 1e-6 * bad.size + 1
+
+
+# ------------------------------------------------------------------ more than 32 sequences
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("B", [33, 64, 700])
+def test_steps_of_many_short_sequences(B, kv):
+    """Batches of more than one block of 32 lengths, some places idle: the fused step's outputs and
+    pages are those of append and step, and the model's."""
+    _, _, rtp = _mods()
+    lens = np.random.default_rng(B).integers(0, 70, B)
+    lens[::7] = 0
+    c = Case(B, lens, 16, kv, G=2, Hkv=3, ret=(True, False, True), window=9, sinks=2)
+    kn, vn = (_bf(c.rng.normal(size=(B, c.Hkv, 128))) for _ in range(2))
+    pools = [x for x in (c.k, c.v, c.k_scale, c.v_scale) if x is not None]
+    first = [x.view(torch.uint8).clone() for x in pools]
+    out, lse = c.outputs()
+    rtp.rtp_paged_decode_step_append(c.desc, c.cache, kn, vn, c.q, c.sl, out, lse, c.ws)
+    assert c.status() == 0
+    fused = [x.view(torch.uint8).clone() for x in pools]
+    for x, y in zip(pools, first):
+        x.view(torch.uint8).copy_(y)
+    slots = [-1 if n == 0 else int(c.table[b, (n - 1) // 16]) * 16 + (n - 1) % 16 for b, n in enumerate(lens)]
+    rtp.rtp_paged_append_kv(c.desc, c.cache, kn, vn, c.sl - 1, _i32(slots), 1, c.ws)
+    out2, lse2 = c.decode()
+    assert c.status() == 0
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+    for x, y in zip(pools, fused):
+        assert torch.equal(x.view(torch.uint8), y)
+    for b, n in enumerate(lens):
+        for g in range(c.Hkv if n else 0):
+            for name, new in (("k", rope_rotate(_f64(kn[b, g]), n - 1, BASE)), ("v", _f64(vn[b, g]))):
+                c.rows[name][b, g][-1] = PO.stored_rows(new, kv)
+    c.check(out, lse)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("append", [False, True])
+def test_steps_of_many_long_sequences(append, kv):
+    """41 sequences of up to 60000 tokens, some places idle, retrieval and local heads: a line long
+    enough to leave ranges to the CTAs done first (bf16), which start in other blocks of 32 lengths.
+    Against 64-bit sums on the GPU; three calls give the same bits."""
+    _, _, rtp = _mods()
+    rng = np.random.default_rng(73)
+    gen = torch.Generator(device=DEV).manual_seed(73)
+    B, G, Hkv, page, sinks, window, ret = 41, 2, 4, 64, 4, 500, [1, 0, 1, 1]
+    lens = rng.integers(1, 60001, B)
+    lens[[0, 13, 31, 32]] = 0
+    assert 3 * (lens / 16).sum() > torch.cuda.get_device_properties(0).multi_processor_count * 8 * 128
+    need = -(-lens // page)
+    n_pages = int(need.sum()) + 1
+    ids, table = rng.permutation(n_pages), np.full((B, need.max()), -1)
+    for b, at in enumerate(np.cumsum(need) - need):
+        table[b, :need[b]] = ids[at:at + need[b]]
+    shape = (n_pages, Hkv, page, 128)
+    pools = {x: torch.randn(shape, dtype=torch.bfloat16, device=DEV, generator=gen) for x in "kv"}
+    scales = dict(k=None, v=None)
+    if kv == "e4m3":
+        for x, p in pools.items():
+            scales[x] = (p.abs().amax(-1).float() / 448.0).contiguous()
+            pools[x] = (p.float() / scales[x][..., None]).to(torch.float8_e4m3fn)
+    bt, sl = _i32(table), _i32(lens)
+    q = (2 * torch.randn((B, G * Hkv, 128), device=DEV, generator=gen)).to(torch.bfloat16)
+    kn, vn = (torch.randn((B, Hkv, 128), device=DEV, generator=gen).to(torch.bfloat16) for _ in range(2))
+    desc = rtp.LayerDesc(B, G * Hkv, Hkv, sinks, window, 1 << 16, rtp.rtp_build_slot_map(ret)[0], BASE)
+    cache = rtp.make_paged_cache(pools["k"], pools["v"], bt, scales["k"], scales["v"])
+    ws = torch.empty(rtp.rtp_paged_workspace_bytes(desc), dtype=torch.uint8, device=DEV)
+    rtp.rtp_paged_workspace_init(ws)
+    outs = []
+    for _ in range(3):
+        out = torch.full((B, G * Hkv, 128), 7.0, dtype=torch.bfloat16, device=DEV)
+        lse = torch.full((B, G * Hkv), 7.0, device=DEV)
+        if append:
+            rtp.rtp_paged_decode_step_append(desc, cache, kn, vn, q, sl, out, lse, ws)
+        else:
+            rtp.rtp_paged_decode_step(desc, cache, q, sl, out, lse, ws)
+        outs.append((out, lse))
+    assert rtp.rtp_read_device_status(ws) == 0 and not ws[:4096].any()
+    for o, l in outs[1:]:
+        assert torch.equal(o, outs[0][0]) and torch.equal(l, outs[0][1])
+    out, lse = outs[0]
+    for b, n in enumerate(lens.tolist()):
+        if n == 0:
+            assert not out[b].any() and (lse[b] == -np.inf).all()
+            continue
+        at = bt[b, :need[b]].long()
+        for g in range(Hkv) if b % 8 == 1 else [b % Hkv]:
+            K, V = (pools[x][at, g].double() if scales[x] is None
+                    else pools[x][at, g].float().double() * scales[x][at, g].double()[..., None] for x in "kv")
+            K, V = K.reshape(-1, 128)[:n], V.reshape(-1, 128)[:n]
+            if append:
+                for x, new in ((K, rope_rotate(_f64(kn[b, g]), n - 1, BASE)), (V, _f64(vn[b, g]))):
+                    assert torch.equal(x[-1].cpu(), torch.from_numpy(PO.stored_rows(new, kv)))
+            pos = torch.from_numpy(PO.positions(n, not ret[g], sinks, window)).to(DEV)
+            K, V = K[pos], V[pos]
+            for h in range(G * g, G * g + G):
+                qr = torch.from_numpy(rope_rotate(_f64(q[b, h]), n - 1, BASE)).to(DEV)
+                z = K @ qr / 128 ** 0.5
+                want, e = torch.softmax(z, 0) @ V, torch.logsumexp(z, 0).item()
+                # as in test_gpu_paged.py, and the e4m3 weights' 2^-31 a row (see above)
+                err = 136 * 2.0 ** -23 * (K.abs() @ qr.abs()).max().item() / 128 ** 0.5
+                rows = len(pos)
+                atol = (2 * err + 2.0 ** -15 + rows / 16 * 2.0 ** -22 + rows * 2.0 ** -31) * V.abs().max().item()
+                d = (out[b, h].double() - want).abs()
+                assert (d <= 2.0 ** -8 * want.abs() + atol).all(), (b, h, d.max().item(), atol)
+                assert abs(lse[b, h].item() - e) <= err + rows / 16 * 2.0 ** -23 + 2.0 ** -21 + 2.0 ** -22 * abs(e)
