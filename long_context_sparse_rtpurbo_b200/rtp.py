@@ -235,6 +235,8 @@ def rtp_paged_workspace_bytes(desc: LayerDesc) -> int:
 
 def rtp_paged_workspace_init(ws: torch.Tensor, stream=None):
     """Once after allocating a workspace of the paged calls (256-byte aligned)."""
+    if ws.get_device() < 0 or ws.get_device() != torch.cuda.current_device():
+        raise ValueError(f"workspace: a tensor on the current device is wanted, got one on {ws.device}")
     return _check("rtp_paged_workspace_init", _lib.load().rtp_paged_workspace_init(
         _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
 

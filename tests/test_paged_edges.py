@@ -94,3 +94,15 @@ def test_binding_is_built_with_the_toolkit_of_nvcc(tmp_path, monkeypatch):
     inner.mkdir(parents=True)
     (inner / "cuda_runtime_api.h").write_text("")
     assert build.cuda_include() == str(inner)
+
+
+def test_workspace_init_refuses_other_devices(monkeypatch):
+    """Host memory, and a device that is not the current one (whose stream would clear it out of order
+    with that device's)."""
+    ws = torch.zeros(4096, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="current device"):
+        rtp.rtp_paged_workspace_init(ws)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 1)
+    with pytest.raises(ValueError, match="current device"):
+        rtp.rtp_paged_workspace_init(ws)
