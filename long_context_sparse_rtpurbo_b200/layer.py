@@ -136,7 +136,8 @@ class PageTable:
         it) and writes the slots of its new tokens to slot_map (int32 [B][n_new]). Updates lens
         in place: a sequence that the free pages do not suffice for keeps its length. step_lens
         then holds the lengths of the sequences that grew and 0 for the others: the seq_lens of
-        the decode step over the new tokens."""
+        the decode step over the new tokens. Further wishes start from lens, not from earlier ones:
+        a sequence that was refused would otherwise grow over positions that nothing wrote."""
         n_new = 0 if slot_map is None else slot_map.shape[1]
         return rtp.rtp_paged_reserve_step(self.pool, self.lens, new_lens, self.counters, self.lens,
                                           self.counters, slot_map, n_new, self.step_lens, self.ws,

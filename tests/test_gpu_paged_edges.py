@@ -126,6 +126,56 @@ def test_a_sequence_that_gets_no_page_is_idle(kv, how):
     assert t.status() == 0 and pl.status() == 0
 
 
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_a_prompt_that_gets_no_pages_stays_out(kv):
+    """Prompts of which the pool holds the first only, then steps of the sequences that the table
+    holds, as README has the loop: the refused ones stay idle when pages become free, until their prompt
+    is reserved again."""
+    _, layer, rtp = _mods()
+    rng = np.random.default_rng(74)
+    B, Hq, Hkv, page, cap = 3, 4, 2, 16, 64
+    t = layer.PageTable(B, 3, page, cap)
+    pl = layer.PagedLayer(t, Hq, Hkv, 2, 20, cap, [1, 0],
+                          torch.bfloat16 if kv == "bf16" else torch.float8_e4m3fn, BASE)
+    for x in (pl.k, pl.v):                                # what nothing wrote is NaN
+        x.view(torch.uint8).fill_(0xFF)
+    lens = np.array([20, 30, 10])
+    new = lambda n, h: _bf(rng.normal(size=(B, n, h, 128)))
+    q, kp, vp = new(30, Hq), new(30, Hkv), new(30, Hkv)
+    slots = torch.empty((B, 30), dtype=torch.int32, device=DEV)
+    out = torch.zeros_like(q)
+
+    def prompts():
+        t.reserve(torch.where(t.lens > 0, t.lens, _i32(lens)), slots)
+        pl.prefill(q, kp, vp, _i32(lens), slots, out)
+
+    def steps(n, live):
+        for _ in range(n):
+            before = t.lens.tolist()
+            t.reserve(t.lens + (t.lens > 0))
+            want = [m + 1 if b in live else 0 for b, m in enumerate(before)]
+            assert t.step_lens.tolist() == want
+            qs, ks, vs = (x[:, 0].contiguous() for x in (new(1, Hq), new(1, Hkv), new(1, Hkv)))
+            o, lse = torch.zeros_like(qs), torch.zeros((B, Hq), device=DEV)
+            pl.decode_append(ks, vs, qs, t.step_lens, o, lse)
+            for b in range(B):
+                if b in live:
+                    assert torch.isfinite(o[b].float()).all() and torch.isfinite(lse[b]).all()
+                else:
+                    assert not o[b].any() and (lse[b] == -np.inf).all()
+
+    prompts()
+    assert t.lens.tolist() == [20, 0, 0]                  # the second lacks a page; nobody passes it
+    steps(3, [0])
+    t.reserve(_i32([0, 0, 0]))
+    steps(2, [])
+    lens[0] = 0
+    prompts()
+    assert t.lens.tolist() == [0, 30, 10]
+    steps(2, [1, 2])
+    assert t.status() == 0 and pl.status() == 0
+
+
 # ------------------------------------------------------------------ one row above a long line
 
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
