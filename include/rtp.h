@@ -344,7 +344,8 @@ int rtp_paged_append_kv(const rtp_layer_desc* desc, const rtp_paged_cache* cache
  *   lse      : float [B][Hq], log sum_j exp(z_j), or NULL.
  *   ws       : rtp_paged_workspace_bytes(desc) bytes or more, initialised.
  * What a page holds outside the attended positions is not used (NaN included). A non-finite
- * value in an attended row makes the outputs of its heads non-finite.
+ * value in an attended row makes the outputs of its heads non-finite; only an infinite key that gives
+ * a head the logit -inf may have the weight 0 there instead.
  * A length out of range (treated as 0) or a page id outside [0, n_pages) (its rows are left out)
  * sets RTP_EDEVICE in ws's status word. Repeated calls give the same bits.
  */

@@ -474,3 +474,31 @@ def test_steps_of_many_long_sequences(append, kv):
                 d = (out[b, h].double() - want).abs()
                 assert (d <= 2.0 ** -8 * want.abs() + atol).all(), (b, h, d.max().item(), atol)
                 assert abs(lse[b, h].item() - e) <= err + rows / 16 * 2.0 ** -23 + 2.0 ** -21 + 2.0 ** -22 * abs(e)
+
+
+# ------------------------------------------------------------------ infinite keys
+
+@pytest.mark.parametrize("value", [float("inf"), float("-inf")])
+def test_heads_of_an_infinite_key(value):
+    """A key with one infinite channel: a head's outputs are non-finite, or, where its logit is -inf,
+    those without the row."""
+    c = Case(75, [40 + b for b in range(8)], 16, "bf16", G=8, Hkv=2, ret=(True, True))
+    rows = [(3 * b) % 40 for b in range(8)]
+    for b, r in enumerate(rows):
+        c.k[int(c.table[b, r // 16]), 0, r % 16, 17 * b % 128] = value
+    out, lse = c.decode()
+    assert c.status() == 0
+    out, lse = _f64(out), _f64(lse)
+    left_out = 0
+    for b, n in enumerate(c.lens):
+        for h in range(c.Hq):
+            if h < c.G and not np.isfinite(out[b, h]).any():
+                assert not np.isfinite(lse[b, h])
+                continue
+            keep = np.delete(np.arange(n), rows[b]) if h < c.G else None
+            left_out += h < c.G
+            if h < c.G:
+                qr = rope_rotate(c.q64[b, h], n - 1, BASE)
+                assert np.sign(qr[17 * b % 128]) != np.sign(value)
+            c.agree(out[b, h], lse[b, h], b, h, n, keep)
+    assert left_out < 32                                  # (a logit of +inf never is)
