@@ -17,8 +17,8 @@
 //
 // Measured (8 KV heads of 4 query heads, all dense; launches back to back): 1M tokens in bf16
 // 627 us, 6.85 TB/s (without the arithmetic 609 us); 4 x 128K tokens in e4m3 187 us, 5.9 TB/s
-// (173 us). Under a load of seconds the power limit takes the clock from 1965 to about 1700 MHz,
-// and e4m3 follows it: 215 us. One sequence of 4K tokens takes 11 us: the chain of lengths, page
+// (173 us). Under a load of seconds the power limit takes the clock from 1965 to about 1700 MHz:
+// 638 to 656 us, and e4m3, which follows the clock, 202 to 217 us. One sequence of 4K tokens takes 11 us: the chain of lengths, page
 // ids, rows, two joins and an arrival, each a trip to L2 or memory.
 #pragma once
 
@@ -596,7 +596,10 @@ __device__ __forceinline__ bool move_ref(const float (&x)[4], float (&m)[2], flo
   return true;
 }
 
-// One tile of 16 rows. Logits S^T = K Q^T, weights as B operand of O^T += V^T P^T (two terms).
+// One tile of 16 rows. Logits S^T = K Q^T, weights as B operand of O^T += V^T P^T in two terms: a
+// weight is off by 2^-17 (two bf16 terms) or 2^-22 (two fp16 terms, and see kLift) of itself, where
+// the output is rounded by up to 2^-8; a third term would be half as many products again. The sum l
+// and the accumulators are in single precision.
 template <int KV>
 __device__ __forceinline__ void paged_tile(PagedAttn<KV>& A, uint32_t stage, uint32_t mask) {
   using Cfg = PagedCfg<KV>;
@@ -1397,8 +1400,11 @@ struct PagedAppendParams {
 // per (token, KV head) row, 4 channel pairs a lane, in double. (Eight CTAs an SM, each at another
 // of these stages; 256 threads and twice the tokens were 2 to 7 % slower.)
 // Bound by HBM: 512 B read, 512 (264) B written per row; bf16 rows run at it (32K tokens of 8 KV
-// heads in 43 us, 6.2 TB/s), e4m3 rows at the issue of instructions (51 us; 300 a row pair, 193
-// for bf16). Single precision with carried errors took twice the instructions.
+// heads in 43 us in graphs, 45 us in a run of calls, 6.0-6.2 TB/s). e4m3 rows (51 us; 300
+// instructions a row pair, 193 for bf16) are bound by the latency of their steps: the issue slots are
+// 59 % busy, and the 29 warps an SM has on average wait for results (2.3 cycles an issue), for the
+// CTA's barriers (1.8) and for conversions and shared memory (1.7). Single precision with
+// carried errors took twice the instructions.
 constexpr int kAppendHeads = 8, kAppendThreads = 128;
 
 template <int KV, int R>
