@@ -25,8 +25,9 @@ def _prefill_scratch(layer, n_max, device, stream):
     if need == 0:
         raise ValueError("librtp rejected the prompt length")
     used = torch.cuda.current_stream(device) if stream is None else stream
-    if not hasattr(used, "cuda_stream"):
-        used = torch.cuda.ExternalStream(int(used), device=device)
+    if not hasattr(used, "cuda_stream"):                  # an address; 0 is the default stream's
+        used = (torch.cuda.ExternalStream(int(used), device=device) if int(used)
+                else torch.cuda.default_stream(device))
     with torch.cuda.stream(used):
         if layer.pf_ws is None or layer.pf_ws.numel() < need:
             layer.pf_ws = _workspace(need, device)

@@ -110,6 +110,26 @@ def test_scratch_comes_from_the_calls_stream(kind, how):
 
 
 @pytest.mark.parametrize("kind", ["contiguous", "paged"])
+def test_address_of_the_default_stream(kind):
+    """The default stream's address is 0: the scratch is marked as used there, not on a new stream."""
+    n = 3000
+    p = Prefill(kind, n)
+    p.run()
+    want = p.results()
+    p.layer.pf_ws = None
+    at = []
+    real = torch.Tensor.record_stream
+    with pytest.MonkeyPatch.context() as m:
+        m.setattr(torch.Tensor, "record_stream", lambda x, s: (at.append(s), real(x, s))[1])
+        p.out.zero_()
+        p.run(torch.cuda.default_stream().cuda_stream)
+    assert torch.cuda.default_stream().cuda_stream == 0
+    assert at == [torch.cuda.default_stream()]
+    assert _same(p.results(), want)
+    p.ok()
+
+
+@pytest.mark.parametrize("kind", ["contiguous", "paged"])
 @pytest.mark.parametrize("warm", [True, False])
 def test_a_graphs_scratch_outlives_a_longer_prompt(kind, warm):
     """A captured prompt, then a longer one that needs more scratch, then tensors of the size of the
